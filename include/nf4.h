@@ -456,6 +456,86 @@ nf4_status_t nf4_linear_group(const void* X, int64_t m, const nf4_weight_t* cons
  */
 int32_t nf4_linear_group_launches(int64_t m, const int64_t* n, int32_t count, int64_t k);
 
+/* ------------------------------------------------------------------------
+ * Integer 4-bit weights with group scales.
+ *
+ * The other common form of 4-bit weights: an integer code per weight, and one
+ * scale (and, if asymmetric, one zero point) for each group of consecutive
+ * weights of a row.  w ~ (q - z) * s.  Same packing as above (two codes per byte,
+ * element 2i in the high nibble of byte i), no double quantization.
+ */
+#define NF4_INT4_WEIGHT_MAGIC 0x49344757u /* "I4GW" */
+
+/*
+ * An integer 4-bit weight W[n, k].  Host struct; the pointers are device pointers
+ * owned by the caller.
+ *   group        weights per scale: 32 or a multiple of 64 that divides k (k itself:
+ *                one scale per row); k % 64 == 0, n <= 2^31 - 1, k < 2^22
+ *   scale_dtype  NF4_BF16 or NF4_F32
+ *   wq           uint8 [n*k/2], 16-byte aligned
+ *   scale        [k/group, n] of scale_dtype: entry [c / group][r] belongs to W[r][c]
+ *   zero         uint8 [k/group, n], values 0 .. 15 (higher bits are ignored), or NULL:
+ *                every zero point is 8
+ */
+typedef struct nf4_int4_weight {
+    uint32_t magic;       /* NF4_INT4_WEIGHT_MAGIC */
+    uint32_t version;     /* NF4_WEIGHT_VERSION */
+    int64_t n;            /* rows (out_features) */
+    int64_t k;            /* columns (in_features) */
+    int64_t group;
+    int32_t scale_dtype;
+    int32_t reserved;     /* 0 */
+    const uint8_t* wq;
+    const void* scale;
+    const uint8_t* zero;
+} nf4_int4_weight_t;
+
+/*
+ * nf4_int4_quantize -- W[n, k] to integer codes with group scales.  Every step is
+ * one fp32 operation rounded to nearest even (rint: halves to even):
+ *   zero == NULL (symmetric):  s = max|w| / 7, z = 8;
+ *   otherwise:  lo = min(w, 0), hi = max(w, 0) over the group, s = (hi - lo) / 15,
+ *               z = clamp(rint(-lo / s), 0, 15);
+ *   s is rounded to scale_dtype first;  q = clamp(rint(w / s) + z, 0, 15).
+ * Where s is 0 the divisions are by 1 (a group of zeros gets q = z).
+ *   W       device, [n, k] of w_dtype, 16-byte aligned
+ *   group, scale_dtype, and the outputs wq, scale, zero as in nf4_int4_weight_t
+ * Errors: NF4_ERR_NULL, NF4_ERR_DTYPE, NF4_ERR_SHAPE, NF4_ERR_ALIGN (W, wq: 16
+ * bytes; scale: its element), NF4_ERR_UNSUPPORTED, NF4_ERR_CUDA.
+ */
+nf4_status_t nf4_int4_quantize(const void* W, nf4_dtype_t w_dtype, int64_t n, int64_t k, int64_t group,
+                               nf4_dtype_t scale_dtype, uint8_t* wq, void* scale, uint8_t* zero,
+                               nf4_stream_t stream);
+
+/*
+ * nf4_int4_dequantize -- out[r][c] = fp32((q - z) * s), rounded to nearest even once
+ * more for out_dtype NF4_BF16.
+ *   out  device, [n, k] of out_dtype, 16-byte aligned  (output)
+ * Errors: NF4_ERR_NULL, NF4_ERR_STATE (magic, version, scale_dtype or reserved),
+ * NF4_ERR_SHAPE, NF4_ERR_ALIGN, NF4_ERR_DTYPE, NF4_ERR_UNSUPPORTED, NF4_ERR_CUDA.
+ */
+nf4_status_t nf4_int4_dequantize(const nf4_int4_weight_t* w, void* out, nf4_dtype_t out_dtype,
+                                 nf4_stream_t stream);
+
+/*
+ * nf4_int4_linear -- Y = X * What^T for an integer 4-bit weight, fused like
+ * nf4_linear.  For m <= 16 the products of X with the integers q - z are exact and
+ * are summed in fp32, and the scale multiplies the sum of each 64 columns (each
+ * group, if it is smaller): What = (q - z) s is never rounded.  For larger m the
+ * weight is restored to bf16 on chip, What = bf16_round(fp32((q - z) s)), and runs on
+ * the dequant-GEMM of nf4_linear.  Sums are in fp32 in an order that does not
+ * depend on timing.
+ *   X          device, bf16 [m, k], 16-byte aligned
+ *   m          rows of X (tokens), >= 1
+ *   Y          device, [m, n] of y_dtype, 16-byte aligned (output)
+ *   dev_status, flags  as for nf4_linear_ex (m <= 16 has no bounded waits:
+ *              NF4_LINEAR_TEST_TIMEOUT is refused there with NF4_ERR_DTYPE)
+ * Errors: as nf4_int4_dequantize; NF4_ERR_SHAPE also for m < 1, NF4_ERR_DTYPE also
+ * for an unknown flag bit.
+ */
+nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* w, void* Y,
+                             nf4_dtype_t y_dtype, int32_t* dev_status, uint32_t flags, nf4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

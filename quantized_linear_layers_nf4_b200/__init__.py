@@ -20,6 +20,10 @@ calls.  Functions carry the C names:
   trained update folded into the weight and quantized again (``merge_lora``
   adds the double quantization and returns an ``NF4Weight``)
 
+* ``nf4_int4_quantize(W, group)`` -> ``(wq, scale, zero)``, ``nf4_int4_dequantize``
+  and ``nf4_int4_linear(X, weight)``: integer 4-bit weights with one scale (and
+  zero point) per group (``int4_quantize_weight`` returns an ``Int4Weight``)
+
 ``quantize_weight(W)`` runs the first two and returns an ``NF4Weight``.  Every
 quantizing call takes ``quant_type="nf4"`` (the default) or ``"fp4"``; an
 ``NF4Weight`` remembers which codebook its codes index.
@@ -32,13 +36,14 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import NF4_BF16, NF4_F32, NF4Error, nf4_weight_t
+from ._lib import NF4_BF16, NF4_F32, NF4Error, nf4_int4_weight_t, nf4_weight_t
 
 __all__ = ["NF4Weight", "NF4Error", "nf4_quantize", "nf4_double_quant", "nf4_dequantize",
            "nf4_linear", "nf4_linear_ex", "nf4_linear_group", "nf4_linear_dx", "nf4_linear_lora", "lora_workspace",
            "nf4_merge_lora", "merge_lora", "nf4_dequantize_batch",
            "nf4_linear_workspace_bytes", "linear_workspace",
-           "quantize_weight", "nf4_codebook", "library_path"]
+           "quantize_weight", "nf4_codebook", "library_path",
+           "Int4Weight", "nf4_int4_quantize", "nf4_int4_dequantize", "nf4_int4_linear", "int4_quantize_weight"]
 
 _DTYPES = {torch.float32: NF4_F32, torch.bfloat16: NF4_BF16}
 _QUANT_TYPES = {"nf4": _lib.NF4_QUANT_NF4, "fp4": _lib.NF4_QUANT_FP4}
@@ -361,3 +366,139 @@ def merge_lora(weight: NF4Weight, down: torch.Tensor, up: torch.Tensor, scale: f
     wq, absmax, _ = nf4_merge_lora(weight, down, up, scale, stream=stream)
     q, s, mu = nf4_double_quant(absmax, stream=stream)
     return NF4Weight(weight.n, weight.k, wq, q, s, mu, weight.quant_type)
+
+
+def _check_out(out: torch.Tensor, shape, dtypes, device, name: str) -> None:
+    if not out.is_cuda or out.device != device or tuple(out.shape) != shape or out.dtype not in dtypes \
+            or not out.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor on %s with one of the dtypes %s"
+                         % (name, shape, device, tuple(dtypes)))
+
+
+def _launch(device: torch.device, stream, fn, where: str, *args) -> None:
+    """fn(*args, stream) on ``device``, which need not be the current one; the
+    stream is that device's current one unless given."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(device, stream, fn, where, *args)
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    st = fn(*args, s)
+    if st != _lib.NF4_OK:
+        _lib.check(st, where)
+
+
+@dataclass(frozen=True)
+class Int4Weight:
+    """An integer 4-bit [n, k] weight with group scales: codes uint8 [n*k/2]
+    (element 2i in the high nibble), ``scale`` [k/group, n] bf16 or fp32 and ``zero``
+    uint8 [k/group, n], or None where every zero point is 8.  W ~ (q - zero) * scale."""
+    n: int
+    k: int
+    group: int
+    wq: torch.Tensor
+    scale: torch.Tensor
+    zero: torch.Tensor | None = None
+
+    def __post_init__(self):
+        n, k, group = self.n, self.k, self.group
+        if n < 1 or k < 1 or group < 1 or k % 64 or (group != 32 and group % 64) or k % group:
+            raise ValueError("k must be a multiple of 64, group 32 or a multiple of 64 that divides k")
+        if not self.wq.is_cuda:
+            raise ValueError("wq must be a CUDA tensor")
+        if self.wq.numel() != n * k // 2:
+            raise ValueError("wq must hold n * k / 2 bytes")
+        dev = self.wq.device
+        _check_out(self.wq, tuple(self.wq.shape), (torch.uint8,), dev, "wq")
+        _check_out(self.scale, (k // group, n), _DTYPES, dev, "scale")
+        if self.zero is not None:
+            _check_out(self.zero, (k // group, n), (torch.uint8,), dev, "zero")
+        st = nf4_int4_weight_t(_lib.NF4_INT4_WEIGHT_MAGIC, _lib.NF4_WEIGHT_VERSION, n, k, group, _DTYPES[self.scale.dtype],
+                               0, self.wq.data_ptr(), self.scale.data_ptr(),
+                               None if self.zero is None else self.zero.data_ptr())
+        object.__setattr__(self, "_struct", st)
+        object.__setattr__(self, "_ref", ctypes.byref(st))
+
+    def struct(self) -> nf4_int4_weight_t:
+        return self._struct
+
+    def nbytes(self) -> int:
+        return (self.wq.numel() + self.scale.numel() * self.scale.element_size() +
+                (0 if self.zero is None else self.zero.numel()))
+
+
+def nf4_int4_quantize(W: torch.Tensor, group: int = 128, symmetric: bool = True, scale_dtype=torch.bfloat16,
+                      wq: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                      zero: torch.Tensor | None = None, stream=None):
+    """Integer codes with one scale per ``group`` weights of a row, for a 2-D fp32/bf16
+    CUDA tensor [n, k].  Returns (wq, scale, zero); zero is None when ``symmetric``."""
+    _need_cuda(W, "W")
+    if W.dim() != 2 or W.dtype not in _DTYPES:
+        raise ValueError("W must be a 2-D float32 or bfloat16 tensor")
+    if scale_dtype not in _DTYPES:
+        raise ValueError("scale_dtype must be float32 or bfloat16")
+    if symmetric and zero is not None:
+        raise ValueError("zero is an output of asymmetric quantization only")
+    n, k = W.shape
+    if group < 1 or k % group or k % 64 or (group != 32 and group % 64):
+        raise ValueError("k must be a multiple of 64, group 32 or a multiple of 64 that divides k")
+    dev = W.device
+    if wq is None:
+        wq = torch.empty(n * k // 2, dtype=torch.uint8, device=dev)
+    if scale is None:
+        scale = torch.empty((k // group, n), dtype=scale_dtype, device=dev)
+    if zero is None and not symmetric:
+        zero = torch.empty((k // group, n), dtype=torch.uint8, device=dev)
+    _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
+    _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
+    if zero is not None:
+        _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
+    _launch(dev, stream, _lib.lib().nf4_int4_quantize, "nf4_int4_quantize", W.data_ptr(), _DTYPES[W.dtype], n, k, group,
+            _DTYPES[scale_dtype], wq.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
+    return wq, scale, zero
+
+
+def int4_quantize_weight(W: torch.Tensor, group: int = 128, symmetric: bool = True, scale_dtype=torch.bfloat16,
+                         stream=None) -> Int4Weight:
+    """nf4_int4_quantize as an Int4Weight."""
+    wq, scale, zero = nf4_int4_quantize(W, group, symmetric, scale_dtype, stream=stream)
+    return Int4Weight(W.shape[0], W.shape[1], group, wq, scale, zero)
+
+
+def nf4_int4_dequantize(weight: Int4Weight, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """(q - zero) * scale as a dense [n, k] tensor of ``dtype`` (of ``out``, where given)."""
+    dev = weight.wq.device
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        out = torch.empty((weight.n, weight.k), dtype=dtype, device=dev)
+    else:
+        _check_out(out, (weight.n, weight.k), _DTYPES, dev, "out")
+    _launch(dev, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._ref, out.data_ptr(),
+            _DTYPES[out.dtype])
+    return out
+
+
+def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                    dev_status: torch.Tensor | None = None, stream=None, weights_early: bool = False,
+                    flags: int = 0) -> torch.Tensor:
+    """Y = X @ W_hat^T for bf16 X [m, k] and an integer 4-bit weight; Y [m, n] in
+    ``dtype`` (in that of ``out``, where given).  Up to 16 tokens the weight is not
+    rounded; above, it is restored to bf16 on chip, as in nf4_linear.
+    ``weights_early`` and ``flags`` as for nf4_linear."""
+    _need_cuda(X, "X")
+    dev = X.device
+    if X.dtype != torch.bfloat16 or X.dim() != 2 or X.shape[1] != weight.k or weight.wq.device != dev:
+        raise ValueError("X must be a 2-D bfloat16 tensor with k columns on the weight's device")
+    m = X.shape[0]
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        out = torch.empty((m, weight.n), dtype=dtype, device=dev)
+    else:
+        _check_out(out, (m, weight.n), _DTYPES, dev, "out")
+    flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
+    _launch(dev, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._ref, out.data_ptr(),
+            _DTYPES[out.dtype], None if dev_status is None else dev_status.data_ptr(), flags)
+    return out

@@ -21,6 +21,7 @@ NF4_WEIGHT_MAGIC = 0x4E463442
 NF4_FP4_WEIGHT_MAGIC = 0x46503442
 NF4_QUANT_NF4 = 0
 NF4_QUANT_FP4 = 1
+NF4_INT4_WEIGHT_MAGIC = 0x49344757
 NF4_WEIGHT_VERSION = 1
 NF4_ABI_VERSION = 1
 NF4_DQ_NOALLOC_MAX_NB = 16777216
@@ -40,6 +41,12 @@ class nf4_weight_t(ctypes.Structure):
     _fields_ = [("magic", ctypes.c_uint32), ("version", ctypes.c_uint32), ("n", _i64), ("k", _i64),
                 ("blocksize", _i32), ("blocksize2", _i32), ("wq", _p), ("absmax_q", _p),
                 ("absmax_scale", _p), ("absmax_offset", _p)]
+
+
+class nf4_int4_weight_t(ctypes.Structure):
+    """Mirror of ``struct nf4_int4_weight``."""
+    _fields_ = [("magic", ctypes.c_uint32), ("version", ctypes.c_uint32), ("n", _i64), ("k", _i64), ("group", _i64),
+                ("scale_dtype", _i32), ("reserved", _i32), ("wq", _p), ("scale", _p), ("zero", _p)]
 
 
 SIGNATURES = {
@@ -72,6 +79,10 @@ SIGNATURES = {
     "nf4_linear_group_launches": (ctypes.c_int32, [_i64, ctypes.POINTER(_i64), ctypes.c_int32, _i64]),
     "nf4_dequantize_batch": (ctypes.c_int, [ctypes.POINTER(ctypes.POINTER(nf4_weight_t)), ctypes.c_int32,
                                             ctypes.POINTER(_p), ctypes.c_int, _p]),
+    "nf4_int4_quantize": (ctypes.c_int, [_p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p, _p]),
+    "nf4_int4_dequantize": (ctypes.c_int, [ctypes.POINTER(nf4_int4_weight_t), _p, ctypes.c_int, _p]),
+    "nf4_int4_linear": (ctypes.c_int, [_p, _i64, ctypes.POINTER(nf4_int4_weight_t), _p, ctypes.c_int, _p,
+                                       ctypes.c_uint32, _p]),
 }
 
 

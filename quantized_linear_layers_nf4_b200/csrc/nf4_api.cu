@@ -71,6 +71,24 @@ nf4_status_t check_weight(const nf4_weight_t* w) {
 // The codebook a (checked) weight's codes index: its magic says NF4 or FP4.
 int codebook_of(const nf4_weight_t* w) { return w->magic == NF4_FP4_WEIGHT_MAGIC ? 1 : 0; }
 
+// Sizes of an integer 4-bit weight; the limits keep an item's group number a single multiply.
+bool int4_shape_ok(int64_t n, int64_t k, int64_t group) {
+    if (n <= 0 || n > INT32_MAX || k <= 0 || k >= (int64_t{1} << 22) || k % 64 != 0) return false;
+    return group > 0 && (group == 32 || group % 64 == 0) && k % group == 0;
+}
+
+nf4_status_t check_int4(const nf4_int4_weight_t* w, nf4::Int4Args* out) {
+    if (!w) return NF4_ERR_NULL;
+    if (w->magic != NF4_INT4_WEIGHT_MAGIC || w->version != NF4_WEIGHT_VERSION || w->reserved != 0 ||
+        (w->scale_dtype != NF4_F32 && w->scale_dtype != NF4_BF16))
+        return NF4_ERR_STATE;
+    if (!w->wq || !w->scale) return NF4_ERR_NULL;
+    if (!int4_shape_ok(w->n, w->k, w->group)) return NF4_ERR_SHAPE;
+    if (!aligned(w->wq, 16) || !aligned(w->scale, w->scale_dtype == NF4_F32 ? 4 : 2)) return NF4_ERR_ALIGN;
+    *out = nf4::Int4Args{w->n, w->k, w->group, w->wq, w->scale, w->zero, w->scale_dtype == NF4_F32};
+    return NF4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -356,6 +374,54 @@ size_t nf4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
 nf4_status_t nf4_linear(const void* X, int64_t m, const nf4_weight_t* w, void* Y,
                         nf4_dtype_t y_dtype, int32_t* dev_status, nf4_stream_t stream) {
     return nf4_linear_ex(X, m, w, Y, y_dtype, dev_status, 0u, stream);
+}
+
+nf4_status_t nf4_int4_quantize(const void* W, nf4_dtype_t w_dtype, int64_t n, int64_t k, int64_t group,
+                               nf4_dtype_t scale_dtype, uint8_t* wq, void* scale, uint8_t* zero,
+                               nf4_stream_t stream) {
+    if (!W || !wq || !scale) return NF4_ERR_NULL;
+    if ((w_dtype != NF4_F32 && w_dtype != NF4_BF16) || (scale_dtype != NF4_F32 && scale_dtype != NF4_BF16))
+        return NF4_ERR_DTYPE;
+    if (!int4_shape_ok(n, k, group)) return NF4_ERR_SHAPE;
+    if (!aligned(W, 16) || !aligned(wq, 16) || !aligned(scale, scale_dtype == NF4_F32 ? 4 : 2)) return NF4_ERR_ALIGN;
+    nf4::DeviceInfo dev;
+    nf4_status_t st = device_ok(&dev);
+    if (st != NF4_OK) return st;
+    return from_cuda(nf4::launch_int4_quantize(W, w_dtype == NF4_BF16, n, k, group, wq, scale, scale_dtype == NF4_F32, zero,
+                                               dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nf4_status_t nf4_int4_dequantize(const nf4_int4_weight_t* w, void* out, nf4_dtype_t out_dtype, nf4_stream_t stream) {
+    nf4::Int4Args a;
+    nf4_status_t st = check_int4(w, &a);
+    if (st != NF4_OK) return st;
+    if (!out) return NF4_ERR_NULL;
+    if (out_dtype != NF4_F32 && out_dtype != NF4_BF16) return NF4_ERR_DTYPE;
+    if (!aligned(out, 16)) return NF4_ERR_ALIGN;
+    nf4::DeviceInfo dev;
+    if ((st = device_ok(&dev)) != NF4_OK) return st;
+    return from_cuda(nf4::launch_int4_dequantize(a, out, out_dtype == NF4_BF16, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* w, void* Y, nf4_dtype_t y_dtype,
+                             int32_t* dev_status, uint32_t flags, nf4_stream_t stream) {
+    nf4::Int4Args a;
+    nf4_status_t st = check_int4(w, &a);
+    if (st != NF4_OK) return st;
+    if (!X || !Y) return NF4_ERR_NULL;
+    if (y_dtype != NF4_F32 && y_dtype != NF4_BF16) return NF4_ERR_DTYPE;
+    const bool few = m <= nf4::kGemvMaxTokens;
+    const uint32_t allowed = few ? NF4_LINEAR_WEIGHTS_EARLY : (NF4_LINEAR_WEIGHTS_EARLY | NF4_LINEAR_TEST_TIMEOUT);
+    if ((flags & ~allowed) != 0) return NF4_ERR_DTYPE;
+    if (m < 1 || m > INT32_MAX / 2) return NF4_ERR_SHAPE;
+    if (!aligned(X, 16) || !aligned(Y, 16) || (dev_status && !aligned(dev_status, 4))) return NF4_ERR_ALIGN;
+    nf4::DeviceInfo dev;
+    if ((st = device_ok(&dev)) != NF4_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (few)
+        return from_cuda(nf4::launch_int4_gemv(X, m, a, Y, y_dtype == NF4_BF16, (flags & NF4_LINEAR_WEIGHTS_EARLY) != 0, dev, s));
+    return from_cuda(nf4::launch_gemm(X, m, a.wq, nullptr, nullptr, nullptr, a.n, a.k, Y, y_dtype == NF4_BF16, dev_status,
+                                      nf4::LoraArgs(), 0, (flags & NF4_LINEAR_TEST_TIMEOUT) ? nf4::kTestStall : 0u, dev, s, &a));
 }
 
 }  // extern "C"

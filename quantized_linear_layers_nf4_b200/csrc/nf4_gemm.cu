@@ -35,6 +35,7 @@
 
 #include "nf4_common.cuh"
 #include "nf4_decode.cuh"
+#include "nf4_few.cuh"
 #include "nf4_internal.h"
 #include "nf4_ptx.cuh"
 #include "nf4_tmap.h"
@@ -74,7 +75,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
-template <bool kBf16Out, bool kLora>
+// kInt4: the codes are integers with group scales instead of codebook levels --
+// 1: groups of whole 64-k stages, 2: groups of 32, two tables per stage.  The
+// 16-entry table of a group is bf16(fp32((j - z) s)), what nf4_int4_dequantize
+// writes; everything else is the same.
+template <bool kBf16Out, bool kLora, int kInt4>
 __global__ void __launch_bounds__(kThreads, 1)
 k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
            const int8_t* __restrict__ absmax_q, const float* __restrict__ absmax_scale,
@@ -82,7 +87,8 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
            int32_t* __restrict__ dev_status, const float* __restrict__ lora_t,
            const __nv_bfloat16* __restrict__ lora_up, int lora_r, int lora_tc,
            const __grid_constant__ CUtensorMap tm_thi, const __grid_constant__ CUtensorMap tm_tlo,
-           const __grid_constant__ CUtensorMap tm_up, int codebook, uint32_t lim, int stall) {
+           const __grid_constant__ CUtensorMap tm_up, int codebook, uint32_t lim, int stall,
+           const few::Int4Sides sides) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -231,10 +237,12 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         const int t = threadIdx.x - 128;  // weight row of the tile
         const int64_t row_c = (n0 + t < n) ? n0 + t : n - 1;  // rows past n: computed, never stored
         const int64_t kblocks = k / 64;
-        const float mu = __ldg(mu_ptr);
+        const float mu = kInt4 ? 0.0f : __ldg(mu_ptr);
         uint64_t cpair[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cpair[j] = pack_f32x2(kCodebook[codebook][2 * j], kCodebook[codebook][2 * j + 1]);
+        for (int j = 0; j < 8; ++j)
+            cpair[j] = kInt4 ? pack_f32x2(2.0f * j, 2.0f * j + 1.0f)
+                             : pack_f32x2(kCodebook[codebook][2 * j], kCodebook[codebook][2 * j + 1]);
         const uint32_t prow = sbase + kOffP + t * 32;
         const uint32_t brow = sbase + kOffB + t * 128;
         const uint32_t swz = static_cast<uint32_t>(t & 7);
@@ -242,7 +250,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         // of 4 consecutive stages are one aligned word and share one scale (a
         // group of 4 blocks never straddles a 256-block boundary); each group is
         // loaded one group ahead so the load latency hides behind 4 stages.
-        const bool grouped = (kblocks & 3) == 0 && (reinterpret_cast<uintptr_t>(absmax_q) & 3) == 0;
+        const bool grouped = !kInt4 && (kblocks & 3) == 0 && (reinterpret_cast<uintptr_t>(absmax_q) & 3) == 0;
         const int64_t rbase = row_c * kblocks;
         uint32_t qw_next = 0, qw_cur = 0;
         float s_next = 0.0f, s_cur = 0.0f;
@@ -250,12 +258,33 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             qw_next = __ldg(reinterpret_cast<const uint32_t*>(absmax_q + rbase));
             s_next = __ldg(absmax_scale + (rbase >> 8));
         }
+        // integer weights: scale and zero point of the stage's group(s), one stage ahead
+        constexpr int kGroups = kInt4 == 2 ? 2 : 1;
+        uint32_t gs[kGroups] = {}, gz[kGroups] = {};
+        auto fetch_sides = [&](int kt) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int64_t at = (kInt4 == 2 ? 2 * static_cast<int64_t>(kt) + i
+                                               : few::group_of(sides, static_cast<uint32_t>(kt))) * n + row_c;
+                gs[i] = few::ldg_scale(sides, at);
+                gz[i] = few::ldg_zero(sides, at);
+            }
+        };
+        if (kInt4) fetch_sides(0);
         for (int kt = 0; kt < nk; ++kt) {
             const int sp = kt % kStagesP;
             const int sb = kt % kStagesB;
-            int q;
-            float sc;
-            if (grouped) {
+            int q = 0;
+            float sc = 0.0f;
+            float iscale[kGroups], izero[kGroups];
+            if (kInt4) {
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    iscale[i] = __uint_as_float(gs[i]);
+                    izero[i] = static_cast<float>(gz[i]);
+                }
+                if (kt + 1 < nk) fetch_sides(kt + 1);
+            } else if (grouped) {
                 if ((kt & 3) == 0) {
                     qw_cur = qw_next;
                     s_cur = s_next;
@@ -279,7 +308,15 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty_p[sp]);
             Planes P;
-            build_planes(cpair, absmax_hat(q, sc, mu), P);
+            auto int4_planes = [&](int i) {
+                const uint64_t off = dup_f32x2(-izero[i]);
+                uint64_t lev[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lev[j]) : "l"(cpair[j]), "l"(off));
+                build_planes(lev, iscale[i], P);
+            };
+            if (kInt4) int4_planes(0);
+            else build_planes(cpair, absmax_hat(q, sc, mu), P);
             if (kt >= kStagesB && !__all_sync(kFull, mbar_wait_n(&empty_b[sb], ((kt / kStagesB) - 1) & 1, lim))) {
                 timed_out = true;
                 break;
@@ -288,6 +325,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             const uint32_t bst = brow + sb * kBBytes;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
+                if (kInt4 == 2 && c == 4) int4_planes(1);
                 const uint32_t x = w[c] ^ 0x88888888u;
                 uint32_t o0, o1, o2, o3;
                 decode4(w[c], x, P, o0, o1);
@@ -636,15 +674,24 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
 cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_t* absmax_q,
                         const float* absmax_scale, const float* absmax_offset, int64_t n, int64_t k, void* Y,
                         bool y_bf16, int32_t* dev_status, const LoraArgs& lora, int codebook,
-                        uint32_t test_flags, const DeviceInfo& dev, cudaStream_t stream) {
-    static bool attr_set[64][4] = {};
+                        uint32_t test_flags, const DeviceInfo& dev, cudaStream_t stream, const Int4Args* w4) {
+    static bool attr_set[64][8] = {};
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     const bool lo = lora.t != nullptr;
-    const void* fn = y_bf16 ? (lo ? reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, true>)
-                                  : reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false>))
-                            : (lo ? reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, true>)
-                                  : reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false>));
-    const int vi = (y_bf16 ? 1 : 0) + (lo ? 2 : 0);
+    const int fmt = !w4 ? 0 : (w4->group == 32 ? 2 : 1);
+    const void* fns[8] = {reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 0>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 0>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, true, 0>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, true, 0>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 1>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 1>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 2>),
+                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 2>)};
+    const int vi = (y_bf16 ? 1 : 0) + (fmt ? 2 + 2 * fmt : (lo ? 2 : 0));
+    const void* fn = fns[vi];
+    few::Int4Sides sides = {};
+    if (w4)
+        sides = few::Int4Sides{w4->scale, w4->zero, w4->n, few::items_magic(w4->group / gemm::kBK), w4->scale_f32 ? 1 : 0};
     {
         static std::mutex mu;
         std::lock_guard<std::mutex> lock(mu);
@@ -681,15 +728,20 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         if (e != cudaSuccess) return e;
         lora_tc = 1;
     }
-#define NF4_GEMM_LAUNCH(B, L)                                                                               \
-    gemm::k_nf4_gemm<B, L><<<grid, gemm::kThreads, gemm::kSmemBytes, stream>>>(                              \
+#define NF4_GEMM_LAUNCH(B, L, F)                                                                               \
+    gemm::k_nf4_gemm<B, L, F><<<grid, gemm::kThreads, gemm::kSmemBytes, stream>>>(                              \
         tm_x, tm_w, absmax_q, absmax_scale, absmax_offset, m, n, k, Y, dev_status, lora.t, lora.up, lora.r,  \
         lora_tc, tm_thi, tm_tlo, tm_up, codebook, (test_flags & kTestStall) ? 64u : kWaitLimit,            \
-        (test_flags & kTestStall) ? 1 : 0)
-    if (y_bf16) {
-        if (lo) NF4_GEMM_LAUNCH(true, true); else NF4_GEMM_LAUNCH(true, false);
-    } else {
-        if (lo) NF4_GEMM_LAUNCH(false, true); else NF4_GEMM_LAUNCH(false, false);
+        (test_flags & kTestStall) ? 1 : 0, sides)
+    switch (vi) {
+        case 0: NF4_GEMM_LAUNCH(false, false, 0); break;
+        case 1: NF4_GEMM_LAUNCH(true, false, 0); break;
+        case 2: NF4_GEMM_LAUNCH(false, true, 0); break;
+        case 3: NF4_GEMM_LAUNCH(true, true, 0); break;
+        case 4: NF4_GEMM_LAUNCH(false, false, 1); break;
+        case 5: NF4_GEMM_LAUNCH(true, false, 1); break;
+        case 6: NF4_GEMM_LAUNCH(false, false, 2); break;
+        default: NF4_GEMM_LAUNCH(true, false, 2); break;
     }
 #undef NF4_GEMM_LAUNCH
     return cudaGetLastError();

@@ -157,10 +157,29 @@ cudaError_t launch_gemm_dx(const void* dY, int64_t m, const uint8_t* wq, const i
                            bool dx_bf16, int32_t* dev_status, int codebook, const DeviceInfo& dev,
                            cudaStream_t stream);
 
+// An integer 4-bit weight with group scales (checked): codes [n, k / 2], scale
+// [k / group, n] (bf16, or fp32 when scale_f32), zero [k / group, n] or null.
+struct Int4Args {
+    int64_t n, k, group;
+    const uint8_t* wq;
+    const void* scale;
+    const uint8_t* zero;
+    bool scale_f32;
+};
+
+// With `w4`, the codes wq are that weight's integers (absmax_* unused, no LoRA).
 cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_t* absmax_q,
                         const float* absmax_scale, const float* absmax_offset, int64_t n, int64_t k, void* Y,
                         bool y_bf16, int32_t* dev_status, const LoraArgs& lora, int codebook,
-                        uint32_t test_flags, const DeviceInfo& dev, cudaStream_t stream);
+                        uint32_t test_flags, const DeviceInfo& dev, cudaStream_t stream,
+                        const Int4Args* w4 = nullptr);
+
+cudaError_t launch_int4_quantize(const void* W, bool w_bf16, int64_t n, int64_t k, int64_t group, uint8_t* wq, void* scale,
+                                 bool scale_f32, uint8_t* zero, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_int4_dequantize(const Int4Args& w, void* out, bool out_bf16, const DeviceInfo& dev, cudaStream_t stream);
+// m <= kGemvMaxTokens; with `early` the weight is read before the preceding kernel is waited for.
+cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early,
+                             const DeviceInfo& dev, cudaStream_t stream);
 
 // Token counts up to this run the decode GEMV; larger ones the tcgen05 GEMM.
 constexpr int64_t kGemvMaxTokens = 16;
