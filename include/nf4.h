@@ -536,6 +536,63 @@ nf4_status_t nf4_int4_dequantize(const nf4_int4_weight_t* w, void* out, nf4_dtyp
 nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* w, void* Y,
                              nf4_dtype_t y_dtype, int32_t* dev_status, uint32_t flags, nf4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Mixture of experts for few tokens.
+ *
+ * The feed-forward layer of a mixture-of-experts decoder with its experts in 4
+ * bits, for decoding: router, choice of the experts, their gated products and the
+ * weighted sum in one call.  For each row x of X:
+ *   l[e] = sum_c x[c] * router[e][c];  the top_k largest, equal ones by the lower e;
+ *   p[e] = exp(l[e] - max l) / sum of the same over all experts
+ *          (over the chosen ones with NF4_MOE_RENORMALIZE);
+ *   y = sum over the chosen e of  D_e ( p[e] * silu(G_e x) * (U_e x) ),  silu(v) = v / (1 + exp(-v)).
+ * An expert's weights are the rows of two stacked weights: gate_up [E * 2f, h] holds
+ * G_e in rows 2 f e .. 2 f e + f - 1 and U_e in the f rows behind them, down [E * h, f]
+ * holds D_e in rows h e .. h e + h - 1.  Weights are used as they stand in their 4 bits,
+ * never rounded to bf16 as products; sums, softmax and activations are fp32, and the
+ * operands of the tensor cores have 11 significant bits (X all of its bits).  The result
+ * does not depend on timing; on the other rows of X it depends in the order of its sums
+ * and the rounding of operands alone.
+ */
+#define NF4_MOE_MAX_EXPERTS 512
+#define NF4_MOE_MAX_TOP_K 16
+
+/* Flag for nf4_moe / nf4_int4_moe: the chosen experts' weights add up to one. */
+#define NF4_MOE_RENORMALIZE 1u
+
+/* Bytes of workspace that nf4_moe and nf4_int4_moe need, for any m; 0 for invalid sizes. */
+size_t nf4_moe_workspace_bytes(int64_t h, int64_t f, int32_t n_experts, int32_t top_k);
+
+/*
+ * nf4_moe -- the layer with NF4 or FP4 experts.
+ *   X          device, bf16 [m, h], 16-byte aligned
+ *   m          tokens, >= 1.  Made for few: they run 16 at a time, each pass reading
+ *              the experts that its tokens chose
+ *   router     device, bf16 [n_experts, h], 16-byte aligned
+ *   n_experts  1 .. NF4_MOE_MAX_EXPERTS
+ *   gate_up    [n_experts * 2f, h];  h % 64 == 0
+ *   down       [n_experts * h, f];   f % 64 == 0
+ *   top_k      1 .. min(n_experts, NF4_MOE_MAX_TOP_K)
+ *   Y          device, bf16 [m, h], 16-byte aligned (output)
+ *   topk_ids   device, int32 [m, top_k] or NULL: the chosen experts, best first (output)
+ *   topk_probs device, fp32 [m, top_k] or NULL: their p (output)
+ *   flags      0 or NF4_MOE_RENORMALIZE
+ *   workspace  device, 16-byte aligned, >= nf4_moe_workspace_bytes(h, f, n_experts, top_k)
+ *              bytes; its contents do not matter.  It must not serve two calls that can
+ *              run at the same time (two streams, two graphs replayed at once).
+ * Errors: NF4_ERR_NULL, NF4_ERR_STATE, NF4_ERR_SHAPE, NF4_ERR_ALIGN, NF4_ERR_DTYPE (unknown
+ * flag), NF4_ERR_WORKSPACE, NF4_ERR_UNSUPPORTED, NF4_ERR_CUDA.
+ */
+nf4_status_t nf4_moe(const void* X, int64_t m, const void* router, int32_t n_experts, const nf4_weight_t* gate_up,
+                     const nf4_weight_t* down, int32_t top_k, void* Y, int32_t* topk_ids, float* topk_probs,
+                     uint32_t flags, void* workspace, size_t ws_bytes, nf4_stream_t stream);
+
+/* nf4_int4_moe -- the same layer with integer 4-bit experts (any groups). */
+nf4_status_t nf4_int4_moe(const void* X, int64_t m, const void* router, int32_t n_experts,
+                          const nf4_int4_weight_t* gate_up, const nf4_int4_weight_t* down, int32_t top_k, void* Y,
+                          int32_t* topk_ids, float* topk_probs, uint32_t flags, void* workspace, size_t ws_bytes,
+                          nf4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

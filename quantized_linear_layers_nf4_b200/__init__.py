@@ -24,6 +24,9 @@ calls.  Functions carry the C names:
   and ``nf4_int4_linear(X, weight)``: integer 4-bit weights with one scale (and
   zero point) per group (``int4_quantize_weight`` returns an ``Int4Weight``)
 
+* ``nf4_moe(X, router, gate_up, down, top_k, workspace=...)``: a mixture-of-experts
+  layer for a few tokens with NF4, FP4 or integer 4-bit experts
+
 ``quantize_weight(W)`` runs the first two and returns an ``NF4Weight``.  Every
 quantizing call takes ``quant_type="nf4"`` (the default) or ``"fp4"``; an
 ``NF4Weight`` remembers which codebook its codes index.
@@ -43,7 +46,8 @@ __all__ = ["NF4Weight", "NF4Error", "nf4_quantize", "nf4_double_quant", "nf4_deq
            "nf4_merge_lora", "merge_lora", "nf4_dequantize_batch",
            "nf4_linear_workspace_bytes", "linear_workspace",
            "quantize_weight", "nf4_codebook", "library_path",
-           "Int4Weight", "nf4_int4_quantize", "nf4_int4_dequantize", "nf4_int4_linear", "int4_quantize_weight"]
+           "Int4Weight", "nf4_int4_quantize", "nf4_int4_dequantize", "nf4_int4_linear", "int4_quantize_weight",
+           "nf4_moe", "moe_workspace"]
 
 _DTYPES = {torch.float32: NF4_F32, torch.bfloat16: NF4_BF16}
 _QUANT_TYPES = {"nf4": _lib.NF4_QUANT_NF4, "fp4": _lib.NF4_QUANT_FP4}
@@ -502,3 +506,61 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
     _launch(dev, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._ref, out.data_ptr(),
             _DTYPES[out.dtype], None if dev_status is None else dev_status.data_ptr(), flags)
     return out
+
+
+def moe_workspace(h: int, f: int, n_experts: int, top_k: int, device=None) -> torch.Tensor:
+    """A workspace for nf4_moe on any number of tokens; its contents do not matter."""
+    nbytes = int(_lib.lib().nf4_moe_workspace_bytes(h, f, n_experts, top_k))
+    if nbytes == 0:
+        raise ValueError("h and f must be multiples of 64, n_experts at most %d, top_k at most %d and n_experts"
+                         % (_lib.NF4_MOE_MAX_EXPERTS, _lib.NF4_MOE_MAX_TOP_K))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def nf4_moe(X: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, renormalize: bool = True,
+            out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+            return_routing: bool = False):
+    """A mixture-of-experts layer for a few tokens: X bf16 [m, h] through router bf16
+    [E, h], the ``top_k`` experts of each row and their gated feed-forward weights,
+    gate_up [E * 2f, h] (each expert's gate rows, then its up rows) and down [E * h, f],
+    both NF4Weight or both Int4Weight.  Returns Y bf16 [m, h], and with
+    ``return_routing`` (Y, ids int32 [m, top_k], probabilities fp32 [m, top_k]).
+    ``workspace`` from ``moe_workspace``; it must not serve two calls at once."""
+    _need_cuda(X, "X")
+    _need_cuda(router, "router")
+    dev = X.device
+    if X.dtype != torch.bfloat16 or X.dim() != 2 or router.dtype != torch.bfloat16 or router.dim() != 2:
+        raise ValueError("X and router must be 2-D bfloat16 tensors")
+    m, h = X.shape
+    n_experts, f = router.shape[0], down.k
+    integer = isinstance(gate_up, Int4Weight)
+    if integer != isinstance(down, Int4Weight):
+        raise ValueError("gate_up and down must both be NF4Weight or both be Int4Weight")
+    if router.shape[1] != h or gate_up.k != h or gate_up.n != n_experts * 2 * f or down.n != n_experts * h:
+        raise ValueError("shapes: X [m, h], router [E, h], gate_up [E * 2f, h], down [E * h, f]")
+    if not (router.device == gate_up.wq.device == down.wq.device == dev):
+        raise ValueError("X, router and the weights must be on one device")
+    if out is None:
+        out = torch.empty_like(X)
+    else:
+        _check_out(out, (m, h), (torch.bfloat16,), dev, "out")
+    if workspace is None:
+        workspace = moe_workspace(h, f, n_experts, top_k, dev)
+        if stream is not None:
+            workspace.record_stream(stream)  # freed here before that stream is done with it
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of X")
+    ids = probs = None
+    if return_routing:
+        ids = torch.empty((m, top_k), dtype=torch.int32, device=dev)
+        probs = torch.empty((m, top_k), dtype=torch.float32, device=dev)
+    L = _lib.lib()
+    if integer:
+        fn, where, gu, dn = L.nf4_int4_moe, "nf4_int4_moe", gate_up._ref, down._ref
+    else:
+        fn, where, gu, dn = L.nf4_moe, "nf4_moe", ctypes.byref(gate_up.struct()), ctypes.byref(down.struct())
+    _launch(dev, stream, fn, where, X.data_ptr(), m, router.data_ptr(), n_experts, gu, dn, top_k, out.data_ptr(),
+            None if ids is None else ids.data_ptr(), None if probs is None else probs.data_ptr(),
+            _lib.NF4_MOE_RENORMALIZE if renormalize else 0, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return (out, ids, probs) if return_routing else out

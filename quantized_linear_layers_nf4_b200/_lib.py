@@ -29,6 +29,9 @@ NF4_LINEAR_WEIGHTS_EARLY = 1
 NF4_LINEAR_TEST_TIMEOUT = 0x80000000
 NF4_LINEAR_GROUP_MAX = 4
 NF4_DEQUANT_BATCH_MAX = 16
+NF4_MOE_MAX_EXPERTS = 512
+NF4_MOE_MAX_TOP_K = 16
+NF4_MOE_RENORMALIZE = 1
 
 # Every function include/nf4.h declares, with (restype, argtypes).
 _p = ctypes.c_void_p
@@ -81,6 +84,12 @@ SIGNATURES = {
                                             ctypes.POINTER(_p), ctypes.c_int, _p]),
     "nf4_int4_quantize": (ctypes.c_int, [_p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p, _p]),
     "nf4_int4_dequantize": (ctypes.c_int, [ctypes.POINTER(nf4_int4_weight_t), _p, ctypes.c_int, _p]),
+    "nf4_moe_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i32, _i32]),
+    "nf4_moe": (ctypes.c_int, [_p, _i64, _p, _i32, ctypes.POINTER(nf4_weight_t), ctypes.POINTER(nf4_weight_t), _i32, _p, _p,
+                               _p, ctypes.c_uint32, _p, ctypes.c_size_t, _p]),
+    "nf4_int4_moe": (ctypes.c_int, [_p, _i64, _p, _i32, ctypes.POINTER(nf4_int4_weight_t),
+                                    ctypes.POINTER(nf4_int4_weight_t), _i32, _p, _p, _p, ctypes.c_uint32, _p,
+                                    ctypes.c_size_t, _p]),
     "nf4_int4_linear": (ctypes.c_int, [_p, _i64, ctypes.POINTER(nf4_int4_weight_t), _p, ctypes.c_int, _p,
                                        ctypes.c_uint32, _p]),
 }

@@ -89,6 +89,37 @@ nf4_status_t check_int4(const nf4_int4_weight_t* w, nf4::Int4Args* out) {
     return NF4_OK;
 }
 
+// What both forms of the mixture-of-experts layer share once their weights are checked.
+nf4_status_t run_moe(const void* X, int64_t m, const void* router, int32_t E, const nf4::MoeWeight& gate_up, int64_t gate_up_n,
+                     const nf4::MoeWeight& down, int64_t down_n, int32_t top_k, void* Y, int32_t* ids, float* probs,
+                     uint32_t flags, void* workspace, size_t ws_bytes, nf4_stream_t stream) {
+    if (!X || !router || !Y) return NF4_ERR_NULL;
+    if ((flags & ~NF4_MOE_RENORMALIZE) != 0) return NF4_ERR_DTYPE;
+    const int64_t h = gate_up.k, f = down.k;
+    if (m < 1 || m > INT32_MAX || nf4_moe_workspace_bytes(h, f, E, top_k) == 0) return NF4_ERR_SHAPE;
+    if (gate_up_n != 2 * f * E || down_n != h * E) return NF4_ERR_SHAPE;
+    if (!aligned(X, 16) || !aligned(router, 16) || !aligned(Y, 16) || (ids && !aligned(ids, 4)) || (probs && !aligned(probs, 4)))
+        return NF4_ERR_ALIGN;
+    if (!workspace || ws_bytes < nf4_moe_workspace_bytes(h, f, E, top_k)) return NF4_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return NF4_ERR_ALIGN;
+    nf4::DeviceInfo dev;
+    nf4_status_t st = device_ok(&dev);
+    if (st != NF4_OK) return st;
+    return from_cuda(nf4::launch_moe(X, m, router, E, gate_up, down, top_k, (flags & NF4_MOE_RENORMALIZE) != 0, Y, ids, probs,
+                                     workspace, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nf4::MoeWeight moe_weight(const nf4_weight_t* w) {
+    nf4::MoeWeight o;
+    o.k = w->k;
+    o.wq = w->wq;
+    o.absmax_q = w->absmax_q;
+    o.absmax_scale = w->absmax_scale;
+    o.absmax_offset = w->absmax_offset;
+    o.codebook = codebook_of(w);
+    return o;
+}
+
 }  // namespace
 
 extern "C" {
@@ -422,6 +453,37 @@ nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* 
         return from_cuda(nf4::launch_int4_gemv(X, m, a, Y, y_dtype == NF4_BF16, (flags & NF4_LINEAR_WEIGHTS_EARLY) != 0, dev, s));
     return from_cuda(nf4::launch_gemm(X, m, a.wq, nullptr, nullptr, nullptr, a.n, a.k, Y, y_dtype == NF4_BF16, dev_status,
                                       nf4::LoraArgs(), 0, (flags & NF4_LINEAR_TEST_TIMEOUT) ? nf4::kTestStall : 0u, dev, s, &a));
+}
+
+size_t nf4_moe_workspace_bytes(int64_t h, int64_t f, int32_t n_experts, int32_t top_k) {
+    constexpr int64_t most = int64_t{1} << 22;
+    if (h < 64 || f < 64 || h % 64 != 0 || f % 64 != 0 || h >= most || f >= most) return 0;
+    if (n_experts < 1 || n_experts > NF4_MOE_MAX_EXPERTS || top_k < 1 || top_k > NF4_MOE_MAX_TOP_K || top_k > n_experts) return 0;
+    return nf4::moe_workspace_bytes(h, f, n_experts, top_k);
+}
+
+nf4_status_t nf4_moe(const void* X, int64_t m, const void* router, int32_t n_experts, const nf4_weight_t* gate_up,
+                     const nf4_weight_t* down, int32_t top_k, void* Y, int32_t* topk_ids, float* topk_probs, uint32_t flags,
+                     void* workspace, size_t ws_bytes, nf4_stream_t stream) {
+    nf4_status_t st = check_weight(gate_up);
+    if (st == NF4_OK) st = check_weight(down);
+    if (st != NF4_OK) return st;
+    return run_moe(X, m, router, n_experts, moe_weight(gate_up), gate_up->n, moe_weight(down), down->n, top_k, Y, topk_ids,
+                   topk_probs, flags, workspace, ws_bytes, stream);
+}
+
+nf4_status_t nf4_int4_moe(const void* X, int64_t m, const void* router, int32_t n_experts, const nf4_int4_weight_t* gate_up,
+                          const nf4_int4_weight_t* down, int32_t top_k, void* Y, int32_t* topk_ids, float* topk_probs,
+                          uint32_t flags, void* workspace, size_t ws_bytes, nf4_stream_t stream) {
+    nf4::MoeWeight gu, dn;
+    nf4_status_t st = check_int4(gate_up, &gu.int4);
+    if (st == NF4_OK) st = check_int4(down, &dn.int4);
+    if (st != NF4_OK) return st;
+    gu.integer = dn.integer = true;
+    gu.k = gate_up->k;
+    dn.k = down->k;
+    return run_moe(X, m, router, n_experts, gu, gate_up->n, dn, down->n, top_k, Y, topk_ids, topk_probs, flags, workspace, ws_bytes,
+                   stream);
 }
 
 }  // extern "C"

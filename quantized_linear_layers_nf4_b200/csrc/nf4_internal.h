@@ -181,6 +181,24 @@ cudaError_t launch_int4_dequantize(const Int4Args& w, void* out, bool out_bf16, 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early,
                              const DeviceInfo& dev, cudaStream_t stream);
 
+// The experts' weights of a mixture-of-experts layer, stacked: integer, or codebook levels.
+struct MoeWeight {
+    int64_t k = 0;
+    bool integer = false;
+    Int4Args int4 = {};
+    const uint8_t* wq = nullptr;
+    const int8_t* absmax_q = nullptr;
+    const float* absmax_scale = nullptr;
+    const float* absmax_offset = nullptr;
+    int codebook = 0;
+};
+size_t moe_workspace_bytes(int64_t h, int64_t f, int E, int top);
+int moe_max_experts();
+int moe_max_top();
+cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, const MoeWeight& gate_up, const MoeWeight& down,
+                       int top, bool renormalize, void* Y, int32_t* ids, float* probs, void* ws, const DeviceInfo& dev,
+                       cudaStream_t stream);
+
 // Token counts up to this run the decode GEMV; larger ones the tcgen05 GEMM.
 constexpr int64_t kGemvMaxTokens = 16;
 
