@@ -71,9 +71,9 @@ nf4_status_t check_weight(const nf4_weight_t* w) {
 // The codebook a (checked) weight's codes index: its magic says NF4 or FP4.
 int codebook_of(const nf4_weight_t* w) { return w->magic == NF4_FP4_WEIGHT_MAGIC ? 1 : 0; }
 
-// Sizes of an integer 4-bit weight; the limits keep an item's group number a single multiply.
+// Sizes of an integer 4-bit weight; k is limited by what a token slab of X takes on chip.
 bool int4_shape_ok(int64_t n, int64_t k, int64_t group) {
-    if (n <= 0 || n > INT32_MAX || k <= 0 || k >= (int64_t{1} << 22) || k % 64 != 0) return false;
+    if (n <= 0 || n > INT32_MAX || k <= 0 || k > 65536 || k % 64 != 0) return false;
     return group > 0 && (group == 32 || group % 64 == 0) && k % group == 0;
 }
 
@@ -456,8 +456,7 @@ nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* 
 }
 
 size_t nf4_moe_workspace_bytes(int64_t h, int64_t f, int32_t n_experts, int32_t top_k) {
-    constexpr int64_t most = int64_t{1} << 22;
-    if (h < 64 || f < 64 || h % 64 != 0 || f % 64 != 0 || h >= most || f >= most) return 0;
+    if (h < 64 || f < 64 || h % 64 != 0 || f % 64 != 0 || h > 65536 || f > 65536) return 0;
     if (n_experts < 1 || n_experts > NF4_MOE_MAX_EXPERTS || top_k < 1 || top_k > NF4_MOE_MAX_TOP_K || top_k > n_experts) return 0;
     return nf4::moe_workspace_bytes(h, f, n_experts, top_k);
 }

@@ -1,0 +1,47 @@
+// nf4_few.cu -- host side that the few-token kernels share (see nf4_few_host.h).
+#include <mutex>
+
+#include "nf4_few_host.h"
+
+namespace nf4 {
+namespace few {
+
+cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& dev, int* out) {
+    struct Known {
+        const void* fn;
+        int device, splits, clusters;
+    };
+    static std::mutex mu;
+    static Known known[1024];
+    static int count = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < count; ++i)
+        if (known[i].fn == fn && known[i].device == dev.device && known[i].splits == splits) {
+            *out = known[i].clusters;
+            return cudaSuccess;
+        }
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    int n = dev.sm_count;
+    if (splits > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / splits * splits));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = kMaxSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+    }
+    if (count < 1024) known[count++] = Known{fn, dev.device, splits, n};
+    *out = n;
+    return cudaSuccess;
+}
+
+}  // namespace few
+}  // namespace nf4

@@ -88,7 +88,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
            const __nv_bfloat16* __restrict__ lora_up, int lora_r, int lora_tc,
            const __grid_constant__ CUtensorMap tm_thi, const __grid_constant__ CUtensorMap tm_tlo,
            const __grid_constant__ CUtensorMap tm_up, int codebook, uint32_t lim, int stall,
-           const few::Int4Sides sides) {
+           const few::Weight sides) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -265,9 +265,9 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 const int64_t at = (kInt4 == 2 ? 2 * static_cast<int64_t>(kt) + i
-                                               : few::group_of(sides, static_cast<uint32_t>(kt))) * n + row_c;
-                gs[i] = few::ldg_scale(sides, at);
-                gz[i] = few::ldg_zero(sides, at);
+                                               : static_cast<int64_t>(kt / sides.per)) * n + row_c;
+                gs[i] = few::ldg_scale(sides.scale, sides.f32, at);
+                gz[i] = sides.zero ? (__ldg(sides.zero + at) & 15u) : 8u;
             }
         };
         if (kInt4) fetch_sides(0);
@@ -689,9 +689,13 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 2>)};
     const int vi = (y_bf16 ? 1 : 0) + (fmt ? 2 + 2 * fmt : (lo ? 2 : 0));
     const void* fn = fns[vi];
-    few::Int4Sides sides = {};
-    if (w4)
-        sides = few::Int4Sides{w4->scale, w4->zero, w4->n, few::items_magic(w4->group / gemm::kBK), w4->scale_f32 ? 1 : 0};
+    few::Weight sides = {};  // scales and zero points
+    if (w4) {
+        sides.scale = w4->scale;
+        sides.zero = w4->zero;
+        sides.per = static_cast<int>(w4->group / gemm::kBK);  // stages of a group
+        sides.f32 = w4->scale_f32 ? 1 : 0;
+    }
     {
         static std::mutex mu;
         std::lock_guard<std::mutex> lock(mu);

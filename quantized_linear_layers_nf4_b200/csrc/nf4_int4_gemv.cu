@@ -3,211 +3,218 @@
 //
 // Bound by HBM: half a byte of code per weight.  The tensor cores (mma.sync: sixteen
 // tokens are too few for a 128-row tcgen05 tile, and the codes would have to pass
-// through shared or tensor memory on the way) multiply the exact integers q - z by X in
-// bf16; the scale goes onto the fp32 sum of each 64-k item (nf4_few.cuh), so nothing is
+// through shared or tensor memory on the way) multiply the exact integers q - z by X,
+// and the scale goes onto the fp32 sum of each group or 128 k (nf4_few.cuh), so nothing is
 // rounded between the codes and the fp32 sums.
 //
-// A CTA has 16 RT rows of W and, with a cluster of S CTAs, a range of k; its eight
-// warps split that range.  Codes go from global memory to registers, kDepth items
-// ahead; X comes through L1.  The warps' sums meet in shared memory and the CTAs' in
-// distributed shared memory, both added in rank order: results do not depend on timing.
+// One CTA an SM.  A cluster of S CTAs has a run of rows, each CTA a range of k of them; the
+// CTA keeps its part of X in shared memory (as fp16, scaled by a power of two per token)
+// and cuts its (16 rows) x (128 k) steps, row tile by row tile, into equal runs for its
+// warps (few::run).  The CTAs' sums are added in rank order through distributed shared
+// memory, so results do not depend on timing.
 #include "nf4_few.cuh"
-#include "nf4_internal.h"
+#include "nf4_few_host.h"
 #include "nf4_ptx.cuh"
 
 namespace nf4 {
 namespace int4 {
 
-constexpr int kWarps = 8;
+using few::kThreads;
+using few::kWarps;
+// Steps on their way in a warp: sixteen tokens' X and sums leave room for three.
+constexpr int depth_of(int nt) { return nt == 1 ? 4 : 3; }
 
-template <bool kG32>
-struct Raw {  // what one item of one 16-row tile brings from memory for a lane
-    uint2 a, b;  // codes of rows g and g + 8
-    uint32_t sa[kG32 ? 2 : 1], sb[kG32 ? 2 : 1], za[kG32 ? 2 : 1], zb[kG32 ? 2 : 1];
+struct GemvArgs {
+    const __nv_bfloat16* x;
+    few::Weight w;
+    void* y;
+    int m, x_lg;            // tokens; warps that bring one token's X in, as a power of two
+    few::Shares rows;       // 8-row groups of W over the clusters
+    few::Shares ks;         // steps of k over a cluster's CTAs
+    int splits;
+    int x_stride;           // bytes of a token's part of X in shared memory
+    int ring_at, slots_at, part_at;  // byte offsets in shared memory
+    int part_rows;
+    int bf16_out, early;
 };
 
-template <int NT, int RT, bool kG32>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-k_int4_gemv(const __nv_bfloat16* __restrict__ X, int m, const uint8_t* __restrict__ wq, const few::Int4Sides sides, int64_t n,
-            int64_t k, void* __restrict__ Y, bool bf16_out, int splits, int early) {
-    constexpr int kDepth = RT >= 4 ? 2 : (RT == 2 ? 3 : 6);
-    constexpr int kRows = 16 * RT, kLd = kRows + 4, kTok = 8 * NT;
-    __shared__ float red[kWarps][kTok][kLd];
-    __shared__ float part[kTok][kLd];
+template <int F, bool Z, int NT>
+__global__ void __launch_bounds__(kThreads, 1) k_int4_gemv(const __grid_constant__ GemvArgs a) {
+    constexpr int kDepth = depth_of(NT);
+    extern __shared__ __align__(128) uint8_t smem[];  // X, the ring, sums of runs, the CTA's sums
+    __shared__ uint32_t top[kWarps];  // bf16 magnitude of a token's largest value in this CTA's range of k
+    float* part = reinterpret_cast<float*>(smem + a.part_at);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / splits) * kRows;
-    const int items = static_cast<int>(k / few::kItemK);
-    const int c0 = static_cast<int>(static_cast<int64_t>(items) * rank / splits);
-    const int c1 = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / splits);
-    const int b0 = c0 + (c1 - c0) * warp / kWarps, b1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
+    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cl = static_cast<int>(blockIdx.x) >> (31 - __clz(a.splits));
+    const int g0 = a.rows.start(cl), g1 = a.rows.start(cl + 1);
+    const int s0 = a.ks.start(rank), ns = a.ks.start(rank + 1) - s0;  // steps of a tile
+    const few::Shares runs = few::shares_of((g1 - g0 + 1) / 2 * ns, kWarps);
+    const uint32_t ring = smem_u32(smem) + a.ring_at + warp * kDepth * few::kStepBytes;
 
-    // byte offset of a lane's codes in a row, and its k, within an item: sixteen k in a
-    // run, or with groups of 32 eight of each group
-    const int coff = kG32 ? 4 * t : 8 * t;
-    const uint8_t* pw[RT][2];
-    int64_t rr[RT][2];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t row = row0 + 16 * r + 8 * i + g;
-            rr[r][i] = row < n ? row : n - 1;  // rows past n: computed, never stored
-            pw[r][i] = wq + rr[r][i] * (k / 2) + coff;
-        }
-    auto fetch = [&](Raw<kG32>(&raw)[RT], int b) {
-        const int64_t off = static_cast<int64_t>(b) * 32;
-        const int64_t gb = kG32 ? 2 * static_cast<int64_t>(b) : few::group_of(sides, static_cast<uint32_t>(b));
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            if (kG32) {
-                raw[r].a = make_uint2(few::ldg_code32(pw[r][0] + off), few::ldg_code32(pw[r][0] + off + 16));
-                raw[r].b = make_uint2(few::ldg_code32(pw[r][1] + off), few::ldg_code32(pw[r][1] + off + 16));
-            } else {
-                raw[r].a = few::ldg_codes(pw[r][0] + off);
-                raw[r].b = few::ldg_codes(pw[r][1] + off);
-            }
-#pragma unroll
-            for (int h = 0; h < (kG32 ? 2 : 1); ++h) {
-                raw[r].sa[h] = few::ldg_scale(sides, (gb + h) * n + rr[r][0]);
-                raw[r].sb[h] = few::ldg_scale(sides, (gb + h) * n + rr[r][1]);
-                raw[r].za[h] = few::ldg_zero(sides, (gb + h) * n + rr[r][0]);
-                raw[r].zb[h] = few::ldg_zero(sides, (gb + h) * n + rr[r][1]);
-            }
+    // the cursor of the loads
+    int left = runs.start(warp + 1) - runs.start(warp);
+    int ft = static_cast<int>(static_cast<unsigned>(runs.start(warp)) / static_cast<unsigned>(ns)), fs = runs.start(warp) - ft * ns;
+    few::Cursor<F, Z> at;
+    auto aim = [&] {
+        const int grp = g0 + ft * 2;
+        // where a run's last tile has one group, that takes the place of another CTA's, and rows
+        // past n are the last one: they are not stored
+        const int64_t r0 = static_cast<int64_t>(grp) * 8 + g, r1 = grp + 1 < g1 ? r0 + 8 : r0;
+        few::aim<F, Z>(at, a.w, r0 < a.w.n ? r0 : a.w.n - 1, r1 < a.w.n ? r1 : a.w.n - 1, s0 + fs, t);
+    };
+    few::Side side[kDepth] = {};
+    const uint32_t put_at = ring + few::ring_place(g, t);
+    auto next = [&](int d) {
+        if (left == 0) return;
+        const bool two = F == few::kG128 || (s0 + fs) * few::kStepK + few::kItemK < a.w.k;
+        few::load_step<F, Z>(side[d], put_at + d * few::kStepBytes, at, a.w, two, t);
+        --left;
+        if (++fs == ns) {
+            fs = 0;
+            ++ft;
+            if (left) aim();
         }
     };
-    float acc[RT][NT][4] = {};
-    auto consume = [&](const Raw<kG32>(&raw)[RT], int b) {
-        uint32_t x[NT][8];
+    if (!a.early) grid_dependency_wait();
+    if (left) aim();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int tok = nt * 8 + g;
-            uint4 u = make_uint4(0, 0, 0, 0), v = u;
-            if (tok < m) {
-                const __nv_bfloat16* xp = X + static_cast<int64_t>(tok) * k + static_cast<int64_t>(b) * few::kItemK + 2 * coff;
-                u = __ldg(reinterpret_cast<const uint4*>(xp));
-                v = __ldg(reinterpret_cast<const uint4*>(xp + (kG32 ? 32 : 8)));
-            }
-            few::pair_x(u.x, u.y, u.z, u.w, *reinterpret_cast<uint32_t(*)[4]>(&x[nt][0]));
-            few::pair_x(v.x, v.y, v.z, v.w, *reinterpret_cast<uint32_t(*)[4]>(&x[nt][4]));
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            float p[NT][4] = {};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int s = kG32 ? h : 0;
-                uint32_t wa[4], wb[4];
-                few::int4_bf16(h ? raw[r].a.y : raw[r].a.x, few::zoff_bf16(raw[r].za[s]), wa);
-                few::int4_bf16(h ? raw[r].b.y : raw[r].b.x, few::zoff_bf16(raw[r].zb[s]), wb);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    few::mma_bf16(p[nt], wa[0], wb[0], wa[1], wb[1], x[nt][4 * h], x[nt][4 * h + 1]);
-                    few::mma_bf16(p[nt], wa[2], wb[2], wa[3], wb[3], x[nt][4 * h + 2], x[nt][4 * h + 3]);
-                }
-                if (kG32 || h == 1) {
-                    const float fa = __uint_as_float(raw[r].sa[s]), fb = __uint_as_float(raw[r].sb[s]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        acc[r][nt][0] = __fmaf_rn(fa, p[nt][0], acc[r][nt][0]);
-                        acc[r][nt][1] = __fmaf_rn(fa, p[nt][1], acc[r][nt][1]);
-                        acc[r][nt][2] = __fmaf_rn(fb, p[nt][2], acc[r][nt][2]);
-                        acc[r][nt][3] = __fmaf_rn(fb, p[nt][3], acc[r][nt][3]);
-                        p[nt][0] = p[nt][1] = p[nt][2] = p[nt][3] = 0.0f;
-                    }
-                }
-            }
-        }
-    };
-
-    Raw<kG32> ring[kDepth][RT];
-    if (!early) grid_dependency_wait();
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-        if (b0 + d < b1) fetch(ring[d], b0 + d);
-    if (early) grid_dependency_wait();
+    for (int d = 0; d < kDepth; ++d) {
+        next(d);
+        few::copies_commit();
+    }
+    if (a.early) grid_dependency_wait();
     grid_launch_dependents();
-    for (int b = b0; b < b1; b += kDepth) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (b + d >= b1) break;
-            consume(ring[d], b + d);
-            if (b + d + kDepth < b1) fetch(ring[d], b + d + kDepth);
-        }
-    }
+    // this CTA's k range of X
+    const int first = s0 * (few::kStepK / 8);
+    few::stage_x<F>(reinterpret_cast<const uint4*>(a.x) + first, a.w.k / 8, min((s0 + ns) * (few::kStepK / 8), a.w.k / 8) - first, a.m,
+                    a.x_lg, smem, a.x_stride, top, warp, lane, kWarps);
 
+    float acc[NT][4] = {};
+    uint32_t xb[NT];  // columns past m read the last token's: their sums are not stored
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float* p0 = &red[warp][nt * 8 + 2 * t][16 * r + g];
-            p0[0] = acc[r][nt][0];
-            p0[kLd] = acc[r][nt][1];
-            p0[8] = acc[r][nt][2];
-            p0[kLd + 8] = acc[r][nt][3];
-        }
-    __syncthreads();
-    auto store = [&](int tok, int r, float v) {
-        const int64_t row = row0 + r;
-        if (tok >= m || row >= n) return;
-        if (bf16_out) reinterpret_cast<__nv_bfloat16*>(Y)[tok * n + row] = __float2bfloat16_rn(v);
-        else reinterpret_cast<float*>(Y)[tok * n + row] = v;
+    for (int nt = 0; nt < NT; ++nt) xb[nt] = smem_u32(smem) + min(nt * 8 + g, a.m - 1) * a.x_stride + few::x_lane<F>(t);
+    auto mul = [&](int d, int step) {
+        const bool two = F == few::kG128 || (s0 + step) * few::kStepK + few::kItemK < a.w.k;
+        few::multiply<F, Z, NT>(side[d], ring + d * few::kStepBytes, a.w, acc, 3, 0.0f, 0u, two, g, t, [&](int j, int nt, uint32_t(&v)[4]) {
+            few::lds128(xb[nt] + step * (few::kStepK * 2) + few::x_word<F>(j, t), v);
+        });
     };
-    for (int i = threadIdx.x; i < kTok * kRows; i += kWarps * 32) {
-        const int tok = i / kRows, r = i % kRows;
-        float v = 0.0f;
+    const int64_t row0 = static_cast<int64_t>(g0) * 8;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(g1 - g0) * 8, a.w.n - row0));
+    auto finish = [&](int tile) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += red[w][tok][r];
-        if (splits == 1) store(tok, r, v);
-        else part[tok][r] = v;
-    }
-    if (splits == 1) return;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int tok = nt * 8 + 2 * t + c;
+                if (tok >= a.m) continue;
+                const float down = few::scale_down(few::scale_exponent(static_cast<int>(top[tok] >> 7)));
+                const int64_t o = tok * a.w.n + row0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = tile * 16 + 8 * i + g;
+                    if (r >= rows) continue;
+                    const float v = acc[nt][2 * i + c] * down;
+                    if (a.splits > 1) part[tok * a.part_rows + r] = v;
+                    else if (a.bf16_out) reinterpret_cast<__nv_bfloat16*>(a.y)[o + r] = __float2bfloat16_rn(v);
+                    else reinterpret_cast<float*>(a.y)[o + r] = v;
+                }
+            }
+    };
+    few::run<kDepth, NT>(acc, reinterpret_cast<float4*>(smem + a.slots_at), warp, lane, runs, ns, next, [](int) {}, mul, finish);
+    if (a.splits == 1) return;
     cluster_sync();
-    const uint32_t base = smem_u32(&part[0][0]);
-    for (int i = threadIdx.x + rank * kWarps * 32; i < kTok * kRows; i += kWarps * 32 * splits) {
-        const int tok = i / kRows, r = i % kRows;
+    const uint32_t base = smem_u32(part);
+    for (int i = threadIdx.x + rank * kThreads; i < a.m * rows; i += kThreads * a.splits) {
+        const int tok = i / rows, r = i - tok * rows;
         float v = 0.0f;
-        for (int s = 0; s < splits; ++s)
-            v += ld_shared_cluster_f32(map_shared_rank(base + (tok * kLd + r) * 4, static_cast<uint32_t>(s)));
-        store(tok, r, v);
+        for (int s = 0; s < a.splits; ++s)
+            v += ld_shared_cluster_f32(map_shared_rank(base + (tok * a.part_rows + r) * 4, static_cast<uint32_t>(s)));
+        if (a.bf16_out) reinterpret_cast<__nv_bfloat16*>(a.y)[tok * a.w.n + row0 + r] = __float2bfloat16_rn(v);
+        else reinterpret_cast<float*>(a.y)[tok * a.w.n + row0 + r] = v;
     }
     cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
+// Shared memory of a pass: X, the ring, sums of runs, and what is left for the CTA's sums.
+struct Room {
+    int64_t x_stride, x, ring, slots, left;
+};
+static Room room_of(int64_t m, int64_t k, int splits, int fmt) {
+    const int nt = m > 8 ? 2 : 1;
+    const int64_t all = (k + few::kStepK - 1) / few::kStepK;
+    Room r;
+    r.x_stride = (all + splits - 1) / splits * few::kStepK * 2 + (fmt == few::kG32 ? few::x_pad<few::kG32>() : few::x_pad<few::kG64>());
+    r.x = (m * r.x_stride + 127) / 128 * 128;
+    r.ring = static_cast<int64_t>(kWarps) * depth_of(nt) * few::kStepBytes;
+    r.slots = static_cast<int64_t>(kWarps) * nt * 512;
+    r.left = few::kMaxSmem - r.x - r.ring - r.slots;
+    return r;
+}
+
 }  // namespace int4
+
+static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early,
+                                         const DeviceInfo& dev, cudaStream_t stream) {
+    using namespace int4;
+    const int nt = m > 8 ? 2 : 1;
+    const int fmt = few::int4_format(w);
+#define NF4_INT4_GEMV(F, Z) reinterpret_cast<const void*>(&k_int4_gemv<F, Z, 1>), reinterpret_cast<const void*>(&k_int4_gemv<F, Z, 2>)
+    static const void* const fns[12] = {NF4_INT4_GEMV(few::kG128, false), NF4_INT4_GEMV(few::kG128, true),
+                                        NF4_INT4_GEMV(few::kG64, false),  NF4_INT4_GEMV(few::kG64, true),
+                                        NF4_INT4_GEMV(few::kG32, false),  NF4_INT4_GEMV(few::kG32, true)};
+#undef NF4_INT4_GEMV
+    const void* fn = fns[(fmt - few::kG128) * 4 + (w.zero ? 2 : 0) + nt - 1];
+    const int64_t all = (w.k + few::kStepK - 1) / few::kStepK;
+    const int64_t groups = (w.n + 7) / 8;
+
+    GemvArgs a = {};
+    // k is split over a cluster where a CTA's share of X would take long to bring in (64 KB),
+    // or where there are fewer row groups than SMs and each part still feeds the warps
+    int splits = 1;
+    while (splits < 8 && (m * w.k * 2 / splits > 64 * 1024 || (groups * splits * 2 <= dev.sm_count && all >= splits * 2 * kWarps))) splits *= 2;
+    const Room at = room_of(m, w.k, splits, fmt);
+    if (at.left < m * 64) return cudaErrorInvalidConfiguration;
+    int fit = 0;
+    cudaError_t e = few::resident(fn, kThreads, splits, dev, &fit);
+    if (e != cudaSuccess) return e;
+    int64_t clusters = fit < groups ? fit : groups;
+    while (splits > 1 && (groups + clusters - 1) / clusters * 8 * m * 4 > at.left) clusters += fit;
+    if (clusters * splits > 0x7fffffff || groups > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    a.x = reinterpret_cast<const __nv_bfloat16*>(X);
+    a.w = few::int4_weight(w);
+    a.y = Y;
+    a.m = static_cast<int>(m);
+    while ((2 << a.x_lg) * m <= kWarps) ++a.x_lg;
+    a.rows = few::shares_of(static_cast<int>(groups), static_cast<int>(clusters));
+    a.ks = few::shares_of(static_cast<int>(all), splits);
+    a.splits = splits;
+    a.x_stride = static_cast<int>(at.x_stride);
+    a.ring_at = static_cast<int>(at.x);
+    a.slots_at = static_cast<int>(at.x + at.ring);
+    a.part_at = static_cast<int>(at.x + at.ring + at.slots);
+    a.part_rows = static_cast<int>((groups + clusters - 1) / clusters * 8);
+    a.bf16_out = y_bf16 ? 1 : 0;
+    a.early = early ? 1 : 0;
+    const size_t smem = static_cast<size_t>(a.part_at + (splits > 1 ? m * a.part_rows * 4 : 0));
+    void* args[1] = {&a};
+    return few::launch(fn, clusters * splits, kThreads, smem, splits, stream, args);
+}
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,
                              cudaStream_t stream) {
-    const int nt = m > 8 ? 2 : 1;
-    const bool g32 = w.group == 32;
-    int rt = m > 4 ? 2 : 1;
-    const int64_t tiles = (w.n + 16 * rt - 1) / (16 * rt);
-    const int64_t items = w.k / few::kItemK;
-    int splits = 1;
-    while (splits < 8 && tiles * splits < dev.sm_count * 2 && items / (splits * 2) >= int4::kWarps * 2) splits *= 2;
-    if (tiles * splits > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    few::Int4Sides s{w.scale, w.zero, w.n, few::items_magic(w.group / few::kItemK), w.scale_f32 ? 1 : 0};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-    cfg.blockDim = dim3(int4::kWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 2 : 1;
-#define NF4_INT4_GEMV(NT, RT, G32)                                                                                             \
-    cudaLaunchKernelEx(&cfg, int4::k_int4_gemv<NT, RT, G32>, reinterpret_cast<const __nv_bfloat16*>(X), static_cast<int>(m),    \
-                       w.wq, s, w.n, w.k, Y, y_bf16, splits, early ? 1 : 0)
-#define NF4_INT4_GEMV_RT(NT, RT) (g32 ? NF4_INT4_GEMV(NT, RT, true) : NF4_INT4_GEMV(NT, RT, false))
-    if (nt == 1) return rt == 1 ? NF4_INT4_GEMV_RT(1, 1) : NF4_INT4_GEMV_RT(1, 2);
-    return rt == 1 ? NF4_INT4_GEMV_RT(2, 1) : NF4_INT4_GEMV_RT(2, 2);
-#undef NF4_INT4_GEMV
-#undef NF4_INT4_GEMV_RT
+    // so many tokens at a time that an eighth of their X leaves room for 16 KB of sums (all
+    // sixteen up to k = 26624, eight to 47104, then four)
+    int64_t most = kGemvMaxTokens;
+    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w)).left < 16 * 1024) most /= 2;
+    for (int64_t t = 0; t < m; t += most) {
+        const cudaError_t e = launch_int4_gemv_pass(static_cast<const char*>(X) + t * w.k * 2, m - t < most ? m - t : most, w,
+                                                    static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, dev, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace nf4

@@ -96,7 +96,7 @@ def _struct(**kw):
 
 
 BAD_STRUCTS = [({"magic": 1}, -5), ({"version": 2}, -5), ({"scale_dtype": 2}, -5), ({"reserved": 1}, -5), ({"wq": None}, -1),
-               ({"scale": None}, -1), ({"n": 0}, -2), ({"n": 1 << 31}, -2), ({"k": 96, "group": 32}, -2), ({"k": 1 << 22}, -2),
+               ({"scale": None}, -1), ({"n": 0}, -2), ({"n": 1 << 31}, -2), ({"k": 96, "group": 32}, -2), ({"k": 65536 + 64}, -2),
                ({"group": 16}, -2), ({"group": 0}, -2), ({"group": -64}, -2), ({"group": 96, "k": 192}, -2),
                ({"group": 512}, -2), ({"wq": FAKE + 8}, -3), ({"scale": FAKE + 1}, -3), ({"scale": FAKE + 2, "scale_dtype": 0}, -3)]
 
@@ -189,7 +189,7 @@ def test_quantize_ties_and_borders(nf4):
 
 # ---------------------------------- linear ----------------------------------
 SHAPES = [(1, 64, 64), (1, 64, 32), (15, 128, 128), (16, 192, 64), (17, 448, 448), (40, 1088, 32), (100, 4096, 128),
-          (1003, 1088, 64), (2048, 640, 320), (129, 16384, 256)]
+          (1003, 1088, 64), (2048, 640, 320), (129, 16384, 256), (8, 65536, 65536), (24, 57344, 32), (9000, 1024, 128), (60001, 128, 64)]
 
 
 @gpu
