@@ -470,7 +470,7 @@ int32_t nf4_linear_group_launches(int64_t m, const int64_t* n, int32_t count, in
  * An integer 4-bit weight W[n, k].  Host struct; the pointers are device pointers
  * owned by the caller.
  *   group        weights per scale: 32 or a multiple of 64 that divides k (k itself:
- *                one scale per row); k % 64 == 0, n <= 2^31 - 1, k <= 65536
+ *                one scale per row); k % 64 == 0, n < 2^30, k <= 65536
  *   scale_dtype  NF4_BF16 or NF4_F32
  *   wq           uint8 [n*k/2], 16-byte aligned
  *   scale        [k/group, n] of scale_dtype: entry [c / group][r] belongs to W[r][c]

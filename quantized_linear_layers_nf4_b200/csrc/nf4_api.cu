@@ -73,7 +73,7 @@ int codebook_of(const nf4_weight_t* w) { return w->magic == NF4_FP4_WEIGHT_MAGIC
 
 // Sizes of an integer 4-bit weight; k is limited by what a token slab of X takes on chip.
 bool int4_shape_ok(int64_t n, int64_t k, int64_t group) {
-    if (n <= 0 || n > INT32_MAX || k <= 0 || k > 65536 || k % 64 != 0) return false;
+    if (n <= 0 || n >= (int64_t{1} << 30) || k <= 0 || k > 65536 || k % 64 != 0) return false;
     return group > 0 && (group == 32 || group % 64 == 0) && k % group == 0;
 }
 

@@ -24,8 +24,9 @@
 //   kG64   groups of 64: 8 consecutive bytes of each half
 //   kG32   groups of 32: 4 consecutive bytes of each quarter
 //   kTable codebook levels with the absmax of each 64: as kG64
-// Scales go to registers: lane (g, t) loads that of group t (kG64, kTable: t % 2) of the step
-// for its rows, and a shuffle hands it to the other lanes of the row.
+// Scales go to registers, four groups of a row at a time (a window: kG128 four steps, kG64 and
+// kTable two, kG32 one): lane (g, t) loads that of group t for its rows, one window ahead, and a
+// shuffle hands it to the other lanes of the row.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -41,8 +42,14 @@ constexpr int kItemK = 64;   // the unit that k is a multiple of
 constexpr int kStepK = 128;  // k of a step; its second half may lie past the end of k
 constexpr int kStepBytes = 16 * kStepK / 2;
 
-constexpr int kWarps = 24;  // of a CTA, one CTA an SM: 80 registers a thread
-constexpr int kThreads = kWarps * 32;
+// Warps of a CTA.  24 fill an SM (80 registers a thread); a call that gives a CTA few steps
+// takes 12, so that the next kernel's CTAs find room and start while its last ones run.
+constexpr int kMaxWarps = 24, kFewWarps = 12;
+constexpr int kFewSteps = 96;  // of a CTA: up to here kFewWarps
+constexpr int kMaxThreads = kMaxWarps * 32;
+
+// The warp's number as a value that the compiler sees to be one for all its lanes.
+__device__ __forceinline__ int warp_index() { return static_cast<int>(__reduce_max_sync(kFull, threadIdx.x >> 5)); }
 
 enum Fmt { kTable = 0, kG128 = 1, kG64 = 2, kG32 = 3 };
 
@@ -138,60 +145,81 @@ struct Weight {
     // integer codes: scale [k / group, n], zero the same or null (then 8)
     const void* scale;
     const uint8_t* zero;
-    int per;         // kG128, kG64: steps, items (of 64 k) of a group
+    uint32_t scale_row;  // bytes of scales of one group
+    int per;         // kG128, kG64: steps, items (of 64 k) of a group; 1
+    int units;       // of a row: kG128 steps, kG64 and kTable items, kG32 groups
     int f32;         // scales are fp32 (bf16 otherwise)
     // codebook codes
     const int8_t* absmax_q;
     const float* absmax_scale;
     const float* mu;
     int codebook;
-    int pairs;       // items 2 i and 2 i + 1 of a row: one aligned pair of absmax codes, one scale
 };
 __device__ __forceinline__ uint32_t ldg_scale(const void* scale, int f32, int64_t at) {  // as fp32 bits
     return f32 ? __ldg(reinterpret_cast<const uint32_t*>(scale) + at)
                : static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(scale) + at)) << 16;
 }
 
-// What goes with a step's codes, as it was loaded: anything done to it before its turn would
-// wait for the load.  For rows g, g + 8.
-struct Side {
-    uint32_t s[2];  // scale; absmax scale
-    uint32_t z[2];  // zero point; absmax code
-};
+// Steps of a window, and groups (kG128: or parts of one) of a step.
+template <int F>
+constexpr int window_steps() { return F == kG128 ? 4 : (F == kG32 ? 1 : 2); }
 
-// Where a lane's two rows are.
+// The scales of a lane's two rows.
 template <int F, bool Z>
-struct Cursor {
-    const uint8_t* c[2];  // the lane's 16 bytes of the next step
-    const uint8_t* s[2];  // its scale; its absmax code
-    const uint8_t* z[2];  // its zero point
-    int64_t e[2];         // kTable: index of its absmax code
-    int left;             // kG128, kG64: steps, items until its next group
-};
+struct Sides {
+    const uint8_t* s[2];  // of the rows' first group; absmax codes
+    const uint8_t* z[2];
+    int64_t e[2];         // kTable: index of the rows' first absmax code
+    uint32_t raw_s[2], raw_z[2];  // of the next window, as loaded: anything done to it would wait for it
+    float f[2];           // of this window
+    uint32_t zz[2];       // zero points of this window, in both halves
 
-template <int F, bool Z>
-__device__ __forceinline__ void aim(Cursor<F, Z>& o, const Weight& w, int64_t row0, int64_t row1, int step, int t) {
-    int grp = 4 * step + t;
-    if (F == kG128 || F == kG64) {
-        const int unit = F == kG128 ? step : 2 * step + (t & 1);
-        grp = static_cast<int>(static_cast<unsigned>(unit) / static_cast<unsigned>(w.per));
-        o.left = w.per - (unit - grp * w.per);
-    }
-    const int items = w.k / kItemK;
+    __device__ __forceinline__ void aim(const Weight& w, const int64_t (&row)[2]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t row = i ? row1 : row0;
-        o.c[i] = w.wq + row * (w.k >> 1) + step * (kStepK / 2) + 16 * t;
-        if (F == kTable) {
-            o.e[i] = row * items + 2 * step + (t & 1);
-            o.s[i] = reinterpret_cast<const uint8_t*>(w.absmax_q) + o.e[i];
-        } else {
-            const int64_t at = grp * w.n + row;
-            o.s[i] = reinterpret_cast<const uint8_t*>(w.scale) + (w.f32 ? 4 * at : 2 * at);
-            if (Z) o.z[i] = w.zero + at;
+        for (int i = 0; i < 2; ++i) {
+            if (F == kTable) {
+                e[i] = row[i] * (w.k / kItemK);
+                s[i] = reinterpret_cast<const uint8_t*>(w.absmax_q) + e[i];
+            } else {
+                s[i] = reinterpret_cast<const uint8_t*>(w.scale) + (w.f32 ? 4 * row[i] : 2 * row[i]);
+                if (Z) z[i] = w.zero + row[i];
+            }
         }
     }
-}
+    __device__ __forceinline__ void load(const Weight& w, int window, int t) {
+        const uint32_t unit = min(4 * window + t, w.units - 1);
+        if (F == kTable) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                raw_z[i] = static_cast<uint32_t>(static_cast<int32_t>(__ldg(reinterpret_cast<const int8_t*>(s[i] + unit))));
+                raw_s[i] = __float_as_uint(__ldg(w.absmax_scale + ((e[i] + unit) >> 8)));
+            }
+            return;
+        }
+        const uint32_t grp = F == kG32 || w.per == 1 ? unit : unit / static_cast<uint32_t>(w.per);
+        const uint64_t to = static_cast<uint64_t>(grp) * w.scale_row;
+        if (w.f32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) raw_s[i] = __ldg(reinterpret_cast<const uint32_t*>(s[i] + to));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) raw_s[i] = __ldg(reinterpret_cast<const uint16_t*>(s[i] + to));
+        }
+        if (Z) {
+            const uint64_t tz = static_cast<uint64_t>(grp) * static_cast<uint32_t>(w.n);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) raw_z[i] = __ldg(z[i] + tz);
+        }
+    }
+    __device__ __forceinline__ void turn(const Weight& w, float mu) {  // the next window becomes this one
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (F == kTable) f[i] = absmax_hat(static_cast<int>(raw_z[i]), __uint_as_float(raw_s[i]), mu);
+            else f[i] = __uint_as_float(raw_s[i] << (w.f32 ? 0 : 16));
+            if (Z) zz[i] = prmt(raw_z[i], 0u, 0x4040) & 0x000f000fu;
+        }
+    }
+};
 
 // The 16-byte chunk c of row r (0 .. 7) of a step in its ring entry: chunks are permuted so that
 // reads of 4, 8 and 16 bytes a lane all find 128 different bytes.
@@ -199,143 +227,93 @@ __device__ __forceinline__ uint32_t ring_place(int r, int c) {
     return 64u * r + 16u * (c ^ (((r >> 1) & 1) << 1 | ((r >> 2) & 1)));
 }
 
-// Starts the copies of the cursor's step into a ring entry (`dst`: the lane's place in it),
-// loads what goes with it, and moves to the next step.  `two`: the step's second half is not
-// past the end of k.
-template <int F, bool Z>
-__device__ __forceinline__ void load_step(Side& o, uint32_t dst, Cursor<F, Z>& at, const Weight& w, bool two, int t) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (F == kG128) copy16(dst + 512 * i, at.c[i]);
-        else copy16(dst + 512 * i, at.c[i], two || t < 2 ? 16 : 0);
-        at.c[i] += kStepK / 2;
-    }
-    if (F == kTable) {
-        const bool in = two || (t & 1) == 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (in) {
-                o.z[i] = static_cast<uint32_t>(static_cast<int32_t>(__ldg(reinterpret_cast<const int8_t*>(at.s[i]))));
-                o.s[i] = __float_as_uint(__ldg(w.absmax_scale + (at.e[i] >> 8)));
-            }
-            at.s[i] += 2;
-            at.e[i] += 2;
-        }
-        return;
-    }
-    const bool in = F == kG128 || two || (F == kG32 ? t < 2 : (t & 1) == 0);
-    const int64_t row_s = w.n << (w.f32 ? 2 : 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (in) {
-            o.s[i] = w.f32 ? __ldg(reinterpret_cast<const uint32_t*>(at.s[i])) : __ldg(reinterpret_cast<const uint16_t*>(at.s[i]));
-            if (Z) o.z[i] = __ldg(at.z[i]);
-        }
-    if (F == kG32) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            at.s[i] += 4 * row_s;
-            if (Z) at.z[i] += 4 * w.n;
-        }
-    } else {
-        at.left -= F == kG128 ? 1 : 2;
-#pragma unroll
-        for (int h = 0; h < (F == kG128 ? 1 : 2); ++h)
-            if (at.left <= 0) {
-                at.left += w.per;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    at.s[i] += row_s;
-                    if (Z) at.z[i] += w.n;
-                }
-            }
-    }
-}
-
 // The two levels of each byte value as fp16, one copy a bank, 256 bytes an entry (the
 // second half of it stays unused), so that a byte in bits 8 .. 15 is an address as it is.
 constexpr int kTableBytes = 256 * 256;
 __device__ __forceinline__ void build_table(uint8_t* tab, int codebook) {
-    for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x) {
-        const int v = i >> 5;
+    for (int i = threadIdx.x; i < 256 * 8; i += blockDim.x) {
+        const int v = i >> 3;
         const __half2 e = __floats2half2_rn(kCodebook[codebook][v >> 4], kCodebook[codebook][v & 15]);
-        *reinterpret_cast<__half2*>(tab + 256 * v + 4 * (i & 31)) = e;
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&e);
+        *reinterpret_cast<uint4*>(tab + 256 * v + 16 * (i & 7)) = make_uint4(u, u, u, u);
     }
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4]) {
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
-}
-
-// The four words of a lane's row g (entry + 512: row g + 8) from a ring entry.
+// The four words of a lane's row g (entry + 512: row g + 8) from a ring entry; `at`: the lane's
+// offsets in it.
+struct Places {
+    uint32_t put;     // where the lane's copies go
+    uint32_t get[4];  // kG128: one; kG64, kTable: of each half; kG32: of each quarter
+};
 template <int F>
-__device__ __forceinline__ void ring_words(uint32_t entry, int g, int t, uint32_t (&v)[4]) {
+__device__ __forceinline__ Places places(int g, int t) {
+    Places o;
+    o.put = ring_place(g, t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        o.get[j] = F == kG128 ? o.put : (F == kG32 ? ring_place(g, j) + 4 * t : ring_place(g, 2 * (j & 1) + (t >> 1)) + 8 * (t & 1));
+    return o;
+}
+template <int F>
+__device__ __forceinline__ void ring_words(const uint8_t* entry, const Places& at, uint32_t (&v)[4]) {
     if (F == kG128) {
-        lds128(entry + ring_place(g, t), v);
+        const uint4 u = *reinterpret_cast<const uint4*>(entry + at.get[0]);
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
     } else if (F == kG32) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = lds32(entry + ring_place(g, j) + 4 * t);
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(entry + at.get[j]);
     } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                         : "=r"(v[2 * h]), "=r"(v[2 * h + 1])
-                         : "r"(entry + ring_place(g, 2 * h + (t >> 1)) + 8 * (t & 1)));
+        for (int h = 0; h < 2; ++h) {
+            const uint2 u = *reinterpret_cast<const uint2*>(entry + at.get[h]);
+            v[2 * h] = u.x;
+            v[2 * h + 1] = u.y;
+        }
     }
 }
 
 // A word as four fp16 pairs; zz: the zero point in both halves; tab: the lane's copy of the table.
 template <int F>
-__device__ __forceinline__ void decode(uint32_t w, uint32_t zz, uint32_t tab, uint32_t (&o)[4]) {
+__device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* tab, uint32_t (&o)[4]) {
     if (F == kTable) {
         const uint32_t v = w >> 16;
-        o[0] = lds32((w & 0xffu) * 256u + tab);
-        o[1] = lds32((w & 0xff00u) + tab);
-        o[2] = lds32((v & 0xffu) * 256u + tab);
-        o[3] = lds32((v & 0xff00u) + tab);
+        o[0] = *reinterpret_cast<const uint32_t*>(tab + (w & 0xffu) * 256u);
+        o[1] = *reinterpret_cast<const uint32_t*>(tab + (w & 0xff00u));
+        o[2] = *reinterpret_cast<const uint32_t*>(tab + (v & 0xffu) * 256u);
+        o[3] = *reinterpret_cast<const uint32_t*>(tab + (v & 0xff00u));
     } else {
         int4_f16(w, zlo_f16(zz), zhi_f16(zz), o);
     }
 }
 
 // acc += (16 rows x 128 k of W) x (128 k x 8 NT columns of X); x(j, nt, v) gives the lane's
-// eight values of word j, column g of n-tile nt; n-tiles without a bit in `live` are left out.
-template <int F, bool Z, int NT, typename XF>
-__device__ __forceinline__ void multiply(const Side& side, uint32_t entry, const Weight& w, float (&acc)[NT][4], int live, float mu,
-                                         uint32_t tab, bool two, int g, int t, XF&& x) {
+// eight values of word j, column g of n-tile nt; n-tiles without a bit in `live` are left out;
+// ahead(j) comes before the first use of word j.  `step`: counted from the row's first.
+template <int F, bool Z, int NT, typename AF, typename XF>
+__device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t* entry, const Places& at, float (&acc)[NT][4], int live,
+                                         const uint8_t* tab, int step, bool two, AF&& ahead, XF&& x) {
     uint32_t c[2][4];
-    ring_words<F>(entry, g, t, c[0]);
-    ring_words<F>(entry + 512, g, t, c[1]);
-    float f[2];
-    uint32_t zz[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (F == kTable) f[i] = absmax_hat(static_cast<int>(side.z[i]), __uint_as_float(side.s[i]), mu);
-        else f[i] = __uint_as_float(side.s[i] << (w.f32 ? 0 : 16));
-        zz[i] = Z ? prmt(side.z[i], 0u, 0x4040) & 0x000f000fu : 0x00080008u;
-    }
-    float p[NT][4];
-    float fj[2] = {f[0], f[1]};
-    uint32_t zj[2] = {zz[0], zz[1]};
+    ring_words<F>(entry, at, c[0]);
+    ring_words<F>(entry + 512, at, c[1]);
+    constexpr int kR = window_steps<F>(), kU = 4 / kR;
+    const int unit = step % kR * kU;  // of the step's first group
+    float p[NT][4], f[2] = {0.0f, 0.0f};
+    uint32_t zz[2] = {0x00080008u, 0x00080008u};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (F != kG128 && j == 2 && !two) return;
+        ahead(j);
         const bool first = F == kG128 ? j == 0 : (F == kG32 || (j & 1) == 0);
         const bool last = F == kG128 ? j == 3 : (F == kG32 || (j & 1) == 1);
-        if (F != kG128 && first) {
+        if (first) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                fj[i] = __shfl_sync(kFull, f[i], F == kG32 ? j : j >> 1, 4);
-                if (Z) zj[i] = __shfl_sync(kFull, zz[i], F == kG32 ? j : j >> 1, 4);
+                f[i] = __shfl_sync(kFull, side.f[i], unit + j * kU / 4, 4);
+                if (Z) zz[i] = __shfl_sync(kFull, side.zz[i], unit + j * kU / 4, 4);
             }
         }
         uint32_t a[4], b[4];
-        decode<F>(c[0][j], zj[0], tab, a);
-        decode<F>(c[1][j], zj[1], tab, b);
+        decode<F>(c[0][j], zz[0], tab, a);
+        decode<F>(c[1][j], zz[1], tab, b);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (NT > 1 && !(live >> nt & 1)) continue;
@@ -349,10 +327,10 @@ __device__ __forceinline__ void multiply(const Side& side, uint32_t entry, const
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (NT > 1 && !(live >> nt & 1)) continue;
-                acc[nt][0] = __fmaf_rn(fj[0], p[nt][0], acc[nt][0]);
-                acc[nt][1] = __fmaf_rn(fj[0], p[nt][1], acc[nt][1]);
-                acc[nt][2] = __fmaf_rn(fj[1], p[nt][2], acc[nt][2]);
-                acc[nt][3] = __fmaf_rn(fj[1], p[nt][3], acc[nt][3]);
+                acc[nt][0] = __fmaf_rn(f[0], p[nt][0], acc[nt][0]);
+                acc[nt][1] = __fmaf_rn(f[0], p[nt][1], acc[nt][1]);
+                acc[nt][2] = __fmaf_rn(f[1], p[nt][2], acc[nt][2]);
+                acc[nt][3] = __fmaf_rn(f[1], p[nt][3], acc[nt][3]);
             }
         }
     }
@@ -378,10 +356,16 @@ template <int F>
 __device__ __forceinline__ uint32_t x_chunk(int j, int t) {  // chunk j itself, counted from the step's first
     return F == kG128 ? 4u * t + j : (F == kG32 ? 4u * j + t : 8u * (j >> 1) + 2u * t + (j & 1));
 }
+// A lane's chunk j of a step lies at x_lane + x_word(j), with x_flip taken off for j >= 2 and added for j < 2.
 template <int F>
-__device__ __forceinline__ uint32_t x_word(int j, int t) {  // and of its chunk j from there
-    return F == kG128 ? 16u * (j ^ (t & 2)) : (F == kG32 ? 64u * j : 128u * (j >> 1) + 16u * (j & 1));
+__device__ __forceinline__ uint32_t x_word(int j) {
+    return F == kG128 ? 16u * j : (F == kG32 ? 64u * j : 128u * (j >> 1) + 16u * (j & 1));
 }
+template <int F>
+__device__ __forceinline__ uint32_t x_flip(int t) {
+    return F == kG128 ? 16u * (t & 2) : 0u;
+}
+
 // X [m] rows of `per` chunks, `row` chunks apart, into shared memory as fp16, each token times the power
 // of two that its largest value here asks for (top[token]: that value's bf16 magnitude), in the order of
 // int4_f16's pairs.  All threads; m is at most the number of warps, which are dealt out evenly to
@@ -446,64 +430,157 @@ __host__ __device__ inline Shares shares_of(int total, int parts) { return Share
 // The steps of a CTA's tiles, one tile's after the other's, are cut into equal runs for
 // its warps.  A tile inside one run is finished from registers; of one that several runs
 // share, the warp that begins it adds the others' sums, in warp order, from `slots`.
-//   next(d)        starts the loads of the run's next step into ring entry d
-//   begin(tile)    as a tile is entered
-//   mul(d, step)   multiplies a step of the tile, which is in entry d
-//   finish(tile)   its sums are complete in acc
-// All threads of the block; the first kDepth steps are already on their way.
-template <int kDepth, int NT, typename Next, typename Begin, typename Mul, typename Finish>
-__device__ __forceinline__ void run(float (&acc)[NT][4], float4* slots, int warp, int lane, const Shares& runs, int ns, Next&& next,
-                                    Begin&& begin, Mul&& mul, Finish&& finish) {
-    const int i0 = runs.start(warp), i1 = runs.start(warp + 1);
-    int tile = static_cast<int>(static_cast<unsigned>(i0) / static_cast<unsigned>(ns)), step = i0 - tile * ns;
-    bool mine = step == 0;  // this warp begins the tile
-    auto put = [&] {
+//   rows(tile, row)      the lane's two rows of a tile
+//   begin(tile)          as a tile is entered
+//   mul(entry, step)     multiplies a step of the tile, counted from the row's first
+//   finish(tile)         its sums are complete in acc
+template <int F, bool Z, int kDepth, int NT>
+struct Runner {
+    static constexpr int kR = window_steps<F>();
+    Sides<F, Z> side;
+    Places places;
+    float acc[NT][4];
+    uint8_t* ring;        // this warp's ring
+    uint32_t put;         // the lane's place in it, as an address
+    int warp, lane, t;
+    int s0, ns;           // steps of a tile: s0 .. s0 + ns of the rows' steps
+    int i0, i1;           // the run
+    int sent, tile, step;  // steps of the run on their way; the next one
+    const uint8_t* c[2];  // the lane's first chunk of the rows of that tile
+    int wtile, window;    // the next window
+
+    template <typename Rows>
+    __device__ __forceinline__ void aim_codes(const Weight& w, Rows&& rows) {
+        int64_t row[2];
+        rows(tile, row);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c[i] = w.wq + row[i] * (w.k >> 1) + 16 * t;
+    }
+    __device__ __forceinline__ bool whole(const Weight& w, int st) const {  // a step's second half is not past the end of k
+        return F == kG128 || (st + 1) * kStepK <= w.k;
+    }
+    template <typename Rows>
+    __device__ __forceinline__ void send(const Weight& w, uint32_t entry, Rows&& rows) {
+        if (sent < i1) {
+            const uint64_t to = static_cast<uint64_t>(static_cast<uint32_t>(step) * (kStepK / 2u));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (F == kG128) copy16(put + entry + 512 * i, c[i] + to);
+                else copy16(put + entry + 512 * i, c[i] + to, whole(w, step) || t < 2 ? 16 : 0);
+            }
+            ++sent;
+            if (++step == s0 + ns) {
+                step = s0;
+                ++tile;
+                if (sent < i1) aim_codes(w, rows);
+            }
+        }
+        copies_commit();
+    }
+    template <typename Rows>
+    __device__ __forceinline__ void next_window(const Weight& w, Rows&& rows) {
+        if (wtile * ns >= i1) return;
+        side.load(w, window, t);
+        if (++window * kR >= s0 + ns) {
+            window = s0 / kR;
+            ++wtile;
+            if (wtile * ns >= i1) return;
+            int64_t row[2];
+            rows(wtile, row);
+            side.aim(w, row);
+        }
+    }
+    // Starts the first loads of the run.
+    template <typename Rows>
+    __device__ __forceinline__ void start(const Weight& w, uint8_t* rings, int warp_, int lane_, const Shares& runs, int s0_, int ns_,
+                                          Rows&& rows) {
+        warp = warp_;
+        lane = lane_;
+        t = lane & 3;
+        s0 = s0_;
+        ns = ns_;
+        places = few::places<F>(lane >> 2, t);
+        ring = rings + warp * kDepth * kStepBytes;
+        put = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + places.put;
+        i0 = sent = runs.start(warp);
+        i1 = runs.start(warp + 1);
+        tile = wtile = ns ? static_cast<int>(static_cast<unsigned>(i0) / static_cast<unsigned>(ns)) : 0;
+        step = s0 + i0 - tile * ns;
+        window = step / kR;
+        if (i0 < i1) {
+            aim_codes(w, rows);
+            int64_t row[2];
+            rows(tile, row);
+            side.aim(w, row);
+        }
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) send(w, d * kStepBytes, rows);
+        if (i0 < i1) next_window(w, rows);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+    }
+    __device__ __forceinline__ void store(float4* slots) const {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) slots[(warp * NT + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-    };
-    if (i0 < i1) begin(tile);
-    for (int i = i0; i < i1; i += kDepth) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (d > 0 && i + d >= i1) break;
-            copies_wait<kDepth - 1>();
-            __syncwarp();
-            mul(d, step);
-            __syncwarp();
-            next(d);
-            copies_commit();
-            if (++step == ns) {
-                if (mine) finish(tile);
-                else put();
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-                mine = true;
-                step = 0;
-                ++tile;
-                if (i + d + 1 < i1) begin(tile);
+    }
+    // All threads of the block; ns > 0.
+    template <typename Rows, typename Begin, typename Mul, typename Finish>
+    __device__ __forceinline__ void run(const Weight& w, float mu, float4* slots, const Shares& runs, Rows&& rows, Begin&& begin, Mul&& mul,
+                                        Finish&& finish) {
+        int tl = static_cast<int>(static_cast<unsigned>(i0) / static_cast<unsigned>(ns)), st = i0 - tl * ns;
+        uint32_t entry = 0;
+        bool mine = st == 0;  // this warp begins the tile
+        for (int i = i0; i < i1;) {
+            begin(tl);
+            const int n = min(ns - st, i1 - i);
+            i += n;
+            side.turn(w, mu);
+            next_window(w, rows);
+            st += s0;
+            for (const int end = st + n;;) {
+                copies_wait<kDepth - 1>();
+                if (F != kG128) __syncwarp();  // else a lane reads what it copied itself
+                mul(ring + entry, st);
+                if (F != kG128) __syncwarp();
+                send(w, entry, rows);
+                entry = entry == (kDepth - 1) * kStepBytes ? 0u : entry + kStepBytes;
+                if (++st == end) break;
+                if (st % kR == 0) {
+                    side.turn(w, mu);
+                    next_window(w, rows);
+                }
             }
+            st -= s0;
+            if (st < ns) break;
+            if (mine) finish(tl);
+            else store(slots);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+            mine = true;
+            st = 0;
+            ++tl;
+        }
+        if (!mine && i0 < i1) store(slots);  // neither begun nor ended here
+        __syncthreads();
+        if (mine && st > 0) {  // begun here, ended by a later warp
+            const int end = (tl + 1) * ns;
+            for (int v = warp + 1, from = i1; from < end; ++v) {
+                const int to = runs.start(v + 1);
+                if (to == from) continue;
+                from = to;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 u = slots[(v * NT + nt) * 32 + lane];
+                    acc[nt][0] += u.x;
+                    acc[nt][1] += u.y;
+                    acc[nt][2] += u.z;
+                    acc[nt][3] += u.w;
+                }
+            }
+            finish(tl);
         }
     }
-    if (!mine && i0 < i1) put();  // neither begun nor ended here
-    __syncthreads();
-    if (mine && step > 0) {  // begun here, ended by a later warp
-        const int end = (tile + 1) * ns;
-        for (int w = warp + 1, from = i1; from < end; ++w) {
-            const int to = runs.start(w + 1);
-            if (to == from) continue;
-            from = to;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float4 v = slots[(w * NT + nt) * 32 + lane];
-                acc[nt][0] += v.x;
-                acc[nt][1] += v.y;
-                acc[nt][2] += v.z;
-                acc[nt][3] += v.w;
-            }
-        }
-        finish(tile);
-    }
-}
+};
 
 }  // namespace few
 }  // namespace nf4

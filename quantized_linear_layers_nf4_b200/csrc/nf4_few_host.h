@@ -12,7 +12,7 @@ constexpr int kMaxSmem = 216 * 1024;  // dynamic shared memory these kernels may
 // Clusters of `splits` (1, 2, 4, 8) CTAs, one CTA an SM, that the current device runs at
 // the same time; also allows the kernel its dynamic shared memory.  Asked of the runtime
 // once per kernel, device and size.
-cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& dev, int* out);
+cudaError_t resident(const void* fn, int splits, const DeviceInfo& dev, int* out);
 
 inline Weight int4_weight(const Int4Args& w) {
     Weight o = {};
@@ -21,6 +21,8 @@ inline Weight int4_weight(const Int4Args& w) {
     o.k = static_cast<int>(w.k);
     o.scale = w.scale;
     o.zero = w.zero;
+    o.scale_row = static_cast<uint32_t>(w.n * (w.scale_f32 ? 4 : 2));
+    o.units = static_cast<int>(w.group == 32 ? w.k / 32 : (w.group % kStepK == 0 ? w.k / kStepK : w.k / kItemK));
     o.per = static_cast<int>(w.group % kStepK == 0 ? w.group / kStepK : w.group / kItemK);
     o.f32 = w.scale_f32 ? 1 : 0;
     return o;

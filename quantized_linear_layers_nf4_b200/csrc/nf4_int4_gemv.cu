@@ -19,8 +19,6 @@
 namespace nf4 {
 namespace int4 {
 
-using few::kThreads;
-using few::kWarps;
 // Steps on their way in a warp: sixteen tokens' X and sums leave room for three.
 constexpr int depth_of(int nt) { return nt == 1 ? 4 : 3; }
 
@@ -39,66 +37,46 @@ struct GemvArgs {
 };
 
 template <int F, bool Z, int NT>
-__global__ void __launch_bounds__(kThreads, 1) k_int4_gemv(const __grid_constant__ GemvArgs a) {
-    constexpr int kDepth = depth_of(NT);
+__global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_constant__ GemvArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];  // X, the ring, sums of runs, the CTA's sums
-    __shared__ uint32_t top[kWarps];  // bf16 magnitude of a token's largest value in this CTA's range of k
+    __shared__ uint32_t top[few::kMaxWarps];  // bf16 magnitude of a token's largest value in this CTA's range of k
     float* part = reinterpret_cast<float*>(smem + a.part_at);
 
-    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = few::warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int cl = static_cast<int>(blockIdx.x) >> (31 - __clz(a.splits));
     const int g0 = a.rows.start(cl), g1 = a.rows.start(cl + 1);
     const int s0 = a.ks.start(rank), ns = a.ks.start(rank + 1) - s0;  // steps of a tile
-    const few::Shares runs = few::shares_of((g1 - g0 + 1) / 2 * ns, kWarps);
-    const uint32_t ring = smem_u32(smem) + a.ring_at + warp * kDepth * few::kStepBytes;
-
-    // the cursor of the loads
-    int left = runs.start(warp + 1) - runs.start(warp);
-    int ft = static_cast<int>(static_cast<unsigned>(runs.start(warp)) / static_cast<unsigned>(ns)), fs = runs.start(warp) - ft * ns;
-    few::Cursor<F, Z> at;
-    auto aim = [&] {
-        const int grp = g0 + ft * 2;
+    const int warps = blockDim.x >> 5;
+    const few::Shares runs = few::shares_of((g1 - g0 + 1) / 2 * ns, warps);
+    auto rows_of = [&](int tile, int64_t(&row)[2]) {
+        const int grp = g0 + tile * 2;
         // where a run's last tile has one group, that takes the place of another CTA's, and rows
         // past n are the last one: they are not stored
-        const int64_t r0 = static_cast<int64_t>(grp) * 8 + g, r1 = grp + 1 < g1 ? r0 + 8 : r0;
-        few::aim<F, Z>(at, a.w, r0 < a.w.n ? r0 : a.w.n - 1, r1 < a.w.n ? r1 : a.w.n - 1, s0 + fs, t);
+        row[0] = min(static_cast<int64_t>(grp) * 8 + g, a.w.n - 1);
+        row[1] = grp + 1 < g1 ? min(static_cast<int64_t>(grp) * 8 + 8 + g, a.w.n - 1) : row[0];
     };
-    few::Side side[kDepth] = {};
-    const uint32_t put_at = ring + few::ring_place(g, t);
-    auto next = [&](int d) {
-        if (left == 0) return;
-        const bool two = F == few::kG128 || (s0 + fs) * few::kStepK + few::kItemK < a.w.k;
-        few::load_step<F, Z>(side[d], put_at + d * few::kStepBytes, at, a.w, two, t);
-        --left;
-        if (++fs == ns) {
-            fs = 0;
-            ++ft;
-            if (left) aim();
-        }
-    };
+    few::Runner<F, Z, depth_of(NT), NT> R;
     if (!a.early) grid_dependency_wait();
-    if (left) aim();
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-        next(d);
-        few::copies_commit();
-    }
+    R.start(a.w, smem + a.ring_at, warp, lane, runs, s0, ns, rows_of);
     if (a.early) grid_dependency_wait();
     grid_launch_dependents();
     // this CTA's k range of X
     const int first = s0 * (few::kStepK / 8);
     few::stage_x<F>(reinterpret_cast<const uint4*>(a.x) + first, a.w.k / 8, min((s0 + ns) * (few::kStepK / 8), a.w.k / 8) - first, a.m,
-                    a.x_lg, smem, a.x_stride, top, warp, lane, kWarps);
+                    a.x_lg, smem, a.x_stride, top, warp, lane, warps);
 
-    float acc[NT][4] = {};
-    uint32_t xb[NT];  // columns past m read the last token's: their sums are not stored
+    const uint8_t* xb[NT][2];  // columns past m read the last token's: their sums are not stored
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xb[nt] = smem_u32(smem) + min(nt * 8 + g, a.m - 1) * a.x_stride + few::x_lane<F>(t);
-    auto mul = [&](int d, int step) {
-        const bool two = F == few::kG128 || (s0 + step) * few::kStepK + few::kItemK < a.w.k;
-        few::multiply<F, Z, NT>(side[d], ring + d * few::kStepBytes, a.w, acc, 3, 0.0f, 0u, two, g, t, [&](int j, int nt, uint32_t(&v)[4]) {
-            few::lds128(xb[nt] + step * (few::kStepK * 2) + few::x_word<F>(j, t), v);
+    for (int nt = 0; nt < NT; ++nt) {
+        xb[nt][0] = smem + min(nt * 8 + g, a.m - 1) * a.x_stride + few::x_lane<F>(t) + few::x_flip<F>(t);
+        xb[nt][1] = xb[nt][0] - 2 * few::x_flip<F>(t);
+    }
+    auto mul = [&](const uint8_t* entry, int step) {
+        const uint32_t x0 = (step - s0) * (few::kStepK * 2);
+        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, 3, nullptr, step, R.whole(a.w, step), [](int) {}, [&](int j, int nt, uint32_t(&v)[4]) {
+            const uint4 u = *reinterpret_cast<const uint4*>(xb[nt][j >> 1] + x0 + few::x_word<F>(j));
+            v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
         });
     };
     const int64_t row0 = static_cast<int64_t>(g0) * 8;
@@ -116,18 +94,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_gemv(const __grid_constant
                 for (int i = 0; i < 2; ++i) {
                     const int r = tile * 16 + 8 * i + g;
                     if (r >= rows) continue;
-                    const float v = acc[nt][2 * i + c] * down;
+                    const float v = R.acc[nt][2 * i + c] * down;
                     if (a.splits > 1) part[tok * a.part_rows + r] = v;
                     else if (a.bf16_out) reinterpret_cast<__nv_bfloat16*>(a.y)[o + r] = __float2bfloat16_rn(v);
                     else reinterpret_cast<float*>(a.y)[o + r] = v;
                 }
             }
     };
-    few::run<kDepth, NT>(acc, reinterpret_cast<float4*>(smem + a.slots_at), warp, lane, runs, ns, next, [](int) {}, mul, finish);
+    R.run(a.w, 0.0f, reinterpret_cast<float4*>(smem + a.slots_at), runs, rows_of, [](int) {}, mul, finish);
     if (a.splits == 1) return;
     cluster_sync();
     const uint32_t base = smem_u32(part);
-    for (int i = threadIdx.x + rank * kThreads; i < a.m * rows; i += kThreads * a.splits) {
+    for (int i = threadIdx.x + rank * blockDim.x; i < a.m * rows; i += blockDim.x * a.splits) {
         const int tok = i / rows, r = i - tok * rows;
         float v = 0.0f;
         for (int s = 0; s < a.splits; ++s)
@@ -142,14 +120,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_gemv(const __grid_constant
 struct Room {
     int64_t x_stride, x, ring, slots, left;
 };
-static Room room_of(int64_t m, int64_t k, int splits, int fmt) {
+static Room room_of(int64_t m, int64_t k, int splits, int fmt, int warps) {
     const int nt = m > 8 ? 2 : 1;
     const int64_t all = (k + few::kStepK - 1) / few::kStepK;
     Room r;
     r.x_stride = (all + splits - 1) / splits * few::kStepK * 2 + (fmt == few::kG32 ? few::x_pad<few::kG32>() : few::x_pad<few::kG64>());
     r.x = (m * r.x_stride + 127) / 128 * 128;
-    r.ring = static_cast<int64_t>(kWarps) * depth_of(nt) * few::kStepBytes;
-    r.slots = static_cast<int64_t>(kWarps) * nt * 512;
+    r.ring = static_cast<int64_t>(warps) * depth_of(nt) * few::kStepBytes;
+    r.slots = static_cast<int64_t>(warps) * nt * 512;
     r.left = few::kMaxSmem - r.x - r.ring - r.slots;
     return r;
 }
@@ -174,20 +152,22 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     // k is split over a cluster where a CTA's share of X would take long to bring in (64 KB),
     // or where there are fewer row groups than SMs and each part still feeds the warps
     int splits = 1;
-    while (splits < 8 && (m * w.k * 2 / splits > 64 * 1024 || (groups * splits * 2 <= dev.sm_count && all >= splits * 2 * kWarps))) splits *= 2;
-    const Room at = room_of(m, w.k, splits, fmt);
-    if (at.left < m * 64) return cudaErrorInvalidConfiguration;
+    while (splits < 8 && (m * w.k * 2 / splits > 64 * 1024 || (groups * splits * 2 <= dev.sm_count && all >= splits * 2 * few::kFewWarps))) splits *= 2;
     int fit = 0;
-    cudaError_t e = few::resident(fn, kThreads, splits, dev, &fit);
+    cudaError_t e = few::resident(fn, splits, dev, &fit);
     if (e != cudaSuccess) return e;
     int64_t clusters = fit < groups ? fit : groups;
+    const int64_t steps = ((groups + clusters - 1) / clusters + 1) / 2 * ((all + splits - 1) / splits);
+    const int warps = steps <= few::kFewSteps && m <= few::kFewWarps ? few::kFewWarps : few::kMaxWarps;  // a warp or more a token for X
+    const Room at = room_of(m, w.k, splits, fmt, warps);
+    if (at.left < m * 64) return cudaErrorInvalidConfiguration;
     while (splits > 1 && (groups + clusters - 1) / clusters * 8 * m * 4 > at.left) clusters += fit;
     if (clusters * splits > 0x7fffffff || groups > 0x7fffffff) return cudaErrorInvalidConfiguration;
     a.x = reinterpret_cast<const __nv_bfloat16*>(X);
     a.w = few::int4_weight(w);
     a.y = Y;
     a.m = static_cast<int>(m);
-    while ((2 << a.x_lg) * m <= kWarps) ++a.x_lg;
+    while ((2 << a.x_lg) * m <= warps) ++a.x_lg;
     a.rows = few::shares_of(static_cast<int>(groups), static_cast<int>(clusters));
     a.ks = few::shares_of(static_cast<int>(all), splits);
     a.splits = splits;
@@ -200,7 +180,7 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     a.early = early ? 1 : 0;
     const size_t smem = static_cast<size_t>(a.part_at + (splits > 1 ? m * a.part_rows * 4 : 0));
     void* args[1] = {&a};
-    return few::launch(fn, clusters * splits, kThreads, smem, splits, stream, args);
+    return few::launch(fn, clusters * splits, warps * 32, smem, splits, stream, args);
 }
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,
@@ -208,7 +188,7 @@ cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* 
     // so many tokens at a time that an eighth of their X leaves room for 16 KB of sums (all
     // sixteen up to k = 26624, eight to 47104, then four)
     int64_t most = kGemvMaxTokens;
-    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w)).left < 16 * 1024) most /= 2;
+    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w), few::kMaxWarps).left < 16 * 1024) most /= 2;
     for (int64_t t = 0; t < m; t += most) {
         const cudaError_t e = launch_int4_gemv_pass(static_cast<const char*>(X) + t * w.k * 2, m - t < most ? m - t : most, w,
                                                     static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, dev, stream);

@@ -34,8 +34,6 @@ constexpr int kMaxTop = 16;
 constexpr int kMaxE = 512;
 constexpr int kMaxPairs = kMaxM * kMaxTop;
 constexpr int kDepth = 3;  // steps on their way in a warp, beside the table of levels
-using few::kThreads;
-using few::kWarps;
 
 struct Params {
     const __nv_bfloat16* x;
@@ -54,11 +52,9 @@ struct Params {
     int32_t* ids;    // [m][top] or null
     float* probs;    // [m][top] or null
     int x_paired, act_paired;  // eight values in the order of int4_f16's pairs
-    int ring_at, slots_at;  // bytes in shared memory: the ring, sums of runs
-    int x_at, x_stride;     // gate and up: X
-    int splits;             // down: CTAs of a cluster; its 8-row groups; the CTAs' sums
-    few::Shares rows;
-    int part_at, part_rows;
+    int ring_at, slots_at;      // bytes in shared memory: the ring, sums of runs
+    few::Shares rows;           // down: 8-row groups of the output over the CTAs
+    int part_at, part_rows;     // down: a pair's products with those rows
 };
 
 // Position of element j of eight in the order (1,5), (0,4), (3,7), (2,6).
@@ -140,12 +136,13 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const __grid_cons
 
 // ------------------------------- routing -------------------------------
 struct Route {
+    uint32_t mask[kMaxE];         // tokens of an expert
+    uint16_t pos[kMaxE];          // of an expert in the list of chosen ones
+    uint16_t list[kMaxPairs];     // chosen experts, ascending
+    uint16_t base[kMaxPairs + 1]; // first pair of a chosen expert; the pairs of an expert are by token
     float prob[kMaxM][kMaxTop];
     uint16_t id[kMaxM][kMaxTop];
-    uint32_t mask[kMaxE];       // tokens of an expert
-    uint16_t pos[kMaxE];        // of an expert in the list of chosen ones
-    uint16_t list[kMaxPairs];   // chosen experts, ascending
-    uint16_t base[kMaxPairs];   // first pair of a chosen expert
+    uint16_t pair[kMaxM][kMaxTop];
     float pair_prob[kMaxPairs];
     uint8_t pair_tok[kMaxPairs];
     int active;
@@ -183,17 +180,18 @@ __device__ __forceinline__ void route(const Params& p, Route& R) {
         for (int j = 0; j < p.top; ++j) {
             uint32_t k = 0;
 #pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i) k = max(k, key[i]);
+            for (int i = 0; i < kMaxE / 32; ++i)
+                if (32 * i < p.E) k = max(k, key[i]);
             const uint32_t kmax = __reduce_max_sync(kFull, k);
             uint32_t at = 0xffffffffu;
 #pragma unroll
             for (int i = kMaxE / 32 - 1; i >= 0; --i)
-                if (key[i] == kmax) at = 32 * i + lane;
+                if (32 * i < p.E && key[i] == kmax) at = 32 * i + lane;
             at = __reduce_min_sync(kFull, at);
             float got = 0.0f;
 #pragma unroll
             for (int i = 0; i < kMaxE / 32; ++i)
-                if (32 * i + lane == static_cast<int>(at)) {
+                if (32 * i < p.E && 32 * i + lane == static_cast<int>(at)) {
                     got = v[i];
                     key[i] = 0;
                 }
@@ -237,37 +235,58 @@ __device__ __forceinline__ void route(const Params& p, Route& R) {
             n += __popc(any);
             pairs += __shfl_sync(kFull, sum, 31);
         }
-        if (lane == 0) R.active = n;
+        if (lane == 0) {
+            R.active = n;
+            R.base[n] = static_cast<uint16_t>(pairs);
+        }
     }
     __syncthreads();
     for (int i = tid; i < p.m * p.top; i += blockDim.x) {
         const int t = i / p.top, j = i % p.top, e = R.id[t][j];
         const int pair = R.base[R.pos[e]] + __popc(R.mask[e] & ((1u << t) - 1));
+        R.pair[t][j] = static_cast<uint16_t>(pair);
         R.pair_prob[pair] = R.prob[t][j];
         R.pair_tok[pair] = static_cast<uint8_t>(t);
     }
     __syncthreads();
 }
 
-// ------------------------------ gate and up ------------------------------
-// XS: X fits in shared memory (else it is read through L1).
-template <int F, bool Z, int NT, bool XS>
-__global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const __grid_constant__ Params p) {
-    extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs, X
-    __shared__ Route R;
-    uint8_t* xsm = smem + p.x_at;
+// Columns of a chosen expert's products are its pairs (token, choice); those past them repeat the
+// last one, and are not used.
+template <int NT>
+struct Columns {
+    int idx = -1, base = 0, cnt = 0, live = 0;  // expert of the list; its pairs; n-tiles with any
+    int pair[NT];                               // of the lane's columns
+    __device__ __forceinline__ bool enter(const Route& R, int i, int g) {
+        if (i == idx) return false;
+        idx = i;
+        base = R.base[i];
+        cnt = R.base[i + 1] - base;
+        live = cnt > 8 ? 3 : 1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) pair[nt] = base + min(nt * 8 + g, cnt - 1);
+        return true;
+    }
+};
 
-    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+// X of a step, from global memory through L1: with one n-tile all of it is asked for before
+// the first word is decoded, with two half of it.
+template <int NT>
+struct Ahead {
+    static constexpr int kWords = NT == 1 ? 4 : 2;
+    uint32_t v[NT][kWords][4];
+};
+
+// ------------------------------ gate and up ------------------------------
+template <int F, bool Z, int NT>
+__global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __grid_constant__ Params p) {
+    extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs
+    __shared__ Route R;
+
+    const int warp = few::warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (F == few::kTable) few::build_table(smem, p.gate_up.codebook);
     grid_dependency_wait();
     grid_launch_dependents();
-    if (XS) {
-        const int per = p.h / 8;
-        for (int tok = 0; tok < p.m; ++tok)
-            for (int c = threadIdx.x; c < per; c += kThreads)
-                *reinterpret_cast<uint4*>(xsm + tok * p.x_stride + few::x_place<F>(c)) =
-                    few::ld_global16(reinterpret_cast<const uint4*>(p.xs + static_cast<int64_t>(tok) * p.h) + c);
-    }
     route(p, R);
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.m * p.top; i += blockDim.x) {
@@ -277,73 +296,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const __grid_consta
 
     const few::Weight& w = p.gate_up;
     const float mu = F == few::kTable ? __ldg(w.mu) : 0.0f;
-    const uint32_t tab = F == few::kTable ? smem_u32(smem) + 4 * lane : 0u;
+    const uint8_t* tab = smem + 4 * lane;
     const int per_e = p.f / 8;
     const few::Shares mine = few::shares_of(R.active * per_e, gridDim.x);
     const int t0 = mine.start(blockIdx.x), t1 = mine.start(blockIdx.x + 1);
     const int ns = (p.h + few::kStepK - 1) / few::kStepK;
-    const few::Shares runs = few::shares_of((t1 - t0) * ns, kWarps);
-    const uint32_t ring = smem_u32(smem) + p.ring_at + warp * kDepth * few::kStepBytes;
+    const few::Shares runs = few::shares_of((t1 - t0) * ns, blockDim.x >> 5);
 
-    int left = runs.start(warp + 1) - runs.start(warp);
-    int ft = static_cast<int>(static_cast<unsigned>(runs.start(warp)) / static_cast<unsigned>(ns)), fs = runs.start(warp) - ft * ns;
-    few::Cursor<F, Z> cur;
-    auto aim = [&] {
-        const int tile = t0 + ft, idx = tile / per_e;
-        const int64_t row = static_cast<int64_t>(R.list[idx]) * 2 * p.f + (tile - idx * per_e) * 8 + g;
-        few::aim<F, Z>(cur, w, row, row + p.f, fs, t);
-    };
-    few::Side side[kDepth] = {};
-    const uint32_t put_at = ring + few::ring_place(g, t);
-    auto next = [&](int d) {
-        if (left == 0) return;
-        const bool two = F == few::kG128 || fs * few::kStepK + few::kItemK < p.h;
-        few::load_step<F, Z>(side[d], put_at + d * few::kStepBytes, cur, w, two, t);
-        --left;
-        if (++fs == ns) {
-            fs = 0;
-            ++ft;
-            if (left) aim();
-        }
-    };
-    if (left) aim();
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-        next(d);
-        few::copies_commit();
-    }
-
-    float acc[NT][4] = {};
-    int at = -1, cnt = 0, live = 0;
-    uint32_t xa[NT];
-    const __half* xg[NT];
-    auto begin = [&](int tile) {
+    auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int idx = (t0 + tile) / per_e;
-        if (idx == at) return;
-        at = idx;
-        cnt = __popc(R.mask[R.list[at]]);
-        live = cnt > 8 ? 3 : 1;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // columns past the expert's tokens read its last one's: their sums are not used
-            const int tok = R.pair_tok[R.base[at] + min(nt * 8 + g, cnt - 1)];
-            xa[nt] = smem_u32(xsm) + tok * p.x_stride + few::x_lane<F>(t);
-            xg[nt] = p.xs + static_cast<int64_t>(tok) * p.h;
-        }
+        row[0] = static_cast<int64_t>(R.list[idx]) * 2 * p.f + (t0 + tile - idx * per_e) * 8 + g;
+        row[1] = row[0] + p.f;
     };
-    auto mul = [&](int d, int step) {
-        const bool two = F == few::kG128 || step * few::kStepK + few::kItemK < p.h;
-        few::multiply<F, Z, NT>(side[d], ring + d * few::kStepBytes, w, acc, live, mu, tab, two, g, t, [&](int j, int nt, uint32_t(&v)[4]) {
-            if (XS) {
-                few::lds128(xa[nt] + step * (few::kStepK * 2) + few::x_word<F>(j, t), v);
-            } else {
-                const uint4 q = few::ld_global16(xg[nt] + step * few::kStepK + few::x_chunk<F>(j, t) * 8);
-                v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-            }
+    few::Runner<F, Z, kDepth, NT> run;
+    run.start(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
+
+    Columns<NT> col;
+    const __half* x[NT];
+    auto begin = [&](int tile) {
+        if (!col.enter(R, (t0 + tile) / per_e, g)) return;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[nt] = p.xs + static_cast<int64_t>(R.pair_tok[col.pair[nt]]) * p.h;
+    };
+    auto mul = [&](const uint8_t* entry, int step) {
+        Ahead<NT> q;
+        constexpr int kW = Ahead<NT>::kWords;
+        const bool two = run.whole(w, step);
+        auto ahead = [&](int j) {
+            if (j % kW != 0) return;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (NT == 1 || (col.live >> nt & 1))
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) {
+                        if (F != few::kG128 && j + i >= 2 && !two) break;
+                        const uint4 u = few::ld_global16(x[nt] + step * few::kStepK + few::x_chunk<F>(j + i, t) * 8);
+                        q.v[nt][i][0] = u.x; q.v[nt][i][1] = u.y; q.v[nt][i][2] = u.z; q.v[nt][i][3] = u.w;
+                    }
+        };
+        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = q.v[nt][j % kW][i];
         });
     };
     auto finish = [&](int tile) {
-        const int r = ((t0 + tile) % per_e) * 8 + g, base = R.base[at];
+        const int r = ((t0 + tile) % per_e) * 8 + g;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -351,92 +348,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const __grid_consta
                 const int j = nt * 8 + 2 * t + c;
                 float a = 0.0f;
                 int tok = 0;
-                if (j < cnt) {
-                    tok = R.pair_tok[base + j];
+                if (j < col.cnt) {
+                    tok = R.pair_tok[col.base + j];
                     const float down = p.xscale[tok];
-                    const float gate = acc[nt][c] * down, up = acc[nt][2 + c] * down;
-                    a = gate / (1.0f + expf(-gate)) * up * R.pair_prob[base + j];
-                    const int64_t o = static_cast<int64_t>(base + j) * p.f;
+                    const float gate = run.acc[nt][c] * down, up = run.acc[nt][2 + c] * down;
+                    a = gate / (1.0f + expf(-gate)) * up * R.pair_prob[col.base + j];
+                    const int64_t o = static_cast<int64_t>(col.base + j) * p.f;
                     const int place = p.act_paired ? (r & ~7) + paired(g) : r;
                     p.act32[o + place] = a;
                     p.act16[o + place] = __float2half_rn(a);
                 }
                 int big = __float_as_int(fabsf(a));
                 for (int s = 4; s < 32; s <<= 1) big = max(big, __shfl_xor_sync(kFull, big, s));
-                if (g == 0 && j < cnt) atomicMax(p.amax + tok, big);
+                if (g == 0 && j < col.cnt) atomicMax(p.amax + tok, big);
             }
     };
-
-    few::run<kDepth, NT>(acc, reinterpret_cast<float4*>(smem + p.slots_at), warp, lane, runs, ns, next, begin, mul, finish);
+    run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, mul, finish);
 }
 
 // --------------------------------- down ---------------------------------
-// As the linear of nf4_int4_gemv.cu, k being the f of every chosen expert one after the
-// other: a cluster has a run of rows, each of its CTAs a range of that k.
+// A CTA has a run of output rows; a tile is 16 of them with one chosen expert's f, its columns that
+// expert's pairs.  The products of a pair go to shared memory, and a token's are added there in the
+// order of its choices.
 template <int F, bool Z, int NT>
-__global__ void __launch_bounds__(kThreads, 1) k_moe_down(const __grid_constant__ Params p) {
-    extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs, the CTA's sums
+__global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_constant__ Params p) {
+    extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs, the pairs' products
     __shared__ Route R;
     __shared__ float factor[kMaxM];
     __shared__ int wide;
     float* part = reinterpret_cast<float*>(smem + p.part_at);
 
-    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = few::warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // The logits are those the previous kernel waited for before it let this one start.
     if (F == few::kTable) few::build_table(smem, p.down.codebook);
     route(p, R);
 
     const few::Weight& w = p.down;
     const float mu = F == few::kTable ? __ldg(w.mu) : 0.0f;
-    const uint32_t tab = F == few::kTable ? smem_u32(smem) + 4 * lane : 0u;
-    const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int cl = static_cast<int>(blockIdx.x) >> (31 - __clz(p.splits));
-    const int g0 = p.rows.start(cl), g1 = p.rows.start(cl + 1);
-    const int per_e = (p.f + few::kStepK - 1) / few::kStepK;
-    const few::Shares ks = few::shares_of(R.active * per_e, p.splits);
-    const int l0 = ks.start(rank), ns = ks.start(rank + 1) - l0;  // steps of a tile
-    const few::Shares runs = few::shares_of((g1 - g0 + 1) / 2 * ns, kWarps);
-    const uint32_t ring = smem_u32(smem) + p.ring_at + warp * kDepth * few::kStepBytes;
+    const uint8_t* tab = smem + 4 * lane;
+    const int g0 = p.rows.start(blockIdx.x), g1 = p.rows.start(blockIdx.x + 1);
+    const int row_tiles = (g1 - g0 + 1) / 2;
+    const int ns = (p.f + few::kStepK - 1) / few::kStepK;
+    const few::Shares runs = few::shares_of(R.active * row_tiles * ns, blockDim.x >> 5);
 
-    int left = runs.start(warp + 1) - runs.start(warp);
-    int ft = ns ? static_cast<int>(static_cast<unsigned>(runs.start(warp)) / static_cast<unsigned>(ns)) : 0, fl = runs.start(warp) - ft * ns;
-    int fe = 0, fs = 0;  // expert of the tile's step fl, and that expert's step
-    few::Cursor<F, Z> cur;
-    auto aim = [&] {
-        const int grp = g0 + ft * 2;
-        const int64_t row = static_cast<int64_t>(R.list[fe]) * p.h + grp * 8 + g;
-        // where the second half is another cluster's, the first takes its place and is not stored
-        few::aim<F, Z>(cur, w, row, row + (grp + 1 < g1 ? 8 : 0), fs, t);
+    auto rows_of = [&](int tile, int64_t(&row)[2]) {
+        const int idx = tile / row_tiles, grp = g0 + (tile - idx * row_tiles) * 2;
+        row[0] = static_cast<int64_t>(R.list[idx]) * p.h + grp * 8 + g;
+        // where the second half is another CTA's, the first takes its place and is not stored
+        row[1] = row[0] + (grp + 1 < g1 ? 8 : 0);
     };
-    auto place = [&] {
-        fe = (l0 + fl) / per_e;
-        fs = l0 + fl - fe * per_e;
-        aim();
-    };
-    few::Side side[kDepth] = {};
-    const uint32_t put_at = ring + few::ring_place(g, t);
-    auto next = [&](int d) {
-        if (left == 0) return;
-        const bool two = F == few::kG128 || fs * few::kStepK + few::kItemK < p.f;
-        few::load_step<F, Z>(side[d], put_at + d * few::kStepBytes, cur, w, two, t);
-        --left;
-        ++fs;
-        if (++fl == ns) {
-            fl = 0;
-            ++ft;
-            if (left) place();
-        } else if (fs == per_e) {
-            fs = 0;
-            ++fe;
-            if (left) aim();
-        }
-    };
-    if (left) place();
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-        next(d);
-        few::copies_commit();
-    }
+    few::Runner<F, Z, kDepth, NT> run;
+    run.start(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -451,82 +413,73 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const __grid_constant_
     __syncthreads();
     const bool conv = wide != 0;
 
-    float acc[NT][4] = {};
-    int at = 0, end = -1, live = 0;  // expert, and the step of the tile that its steps end before
-    bool col[NT];
+    Columns<NT> col;
     int64_t off[NT];
     float fct[NT];
-    auto mul = [&](int d, int l) {
-        if (l >= end || l == 0) {
-            at = (l0 + l) / per_e;
-            end = (at + 1) * per_e - l0;
-            const uint32_t mask = R.mask[R.list[at]];
-            live = 0;
+    auto begin = [&](int tile) {
+        if (!col.enter(R, tile / row_tiles, g)) return;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int tok = nt * 8 + g;
-                if (mask >> (8 * nt) & 0xffu) live |= 1 << nt;
-                col[nt] = mask >> tok & 1;
-                // counted from the tile's first step
-                off[nt] = static_cast<int64_t>(R.base[at] + __popc(mask & ((1u << tok) - 1))) * p.f + static_cast<int64_t>(l0 - at * per_e) * few::kStepK;
-                fct[nt] = factor[tok < p.m ? tok : 0];
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+            off[nt] = static_cast<int64_t>(col.pair[nt]) * p.f;
+            fct[nt] = factor[R.pair_tok[col.pair[nt]]];
         }
-        const bool two = F == few::kG128 || (l0 + l - at * per_e) * few::kStepK + few::kItemK < p.f;
-        few::multiply<F, Z, NT>(side[d], ring + d * few::kStepBytes, w, acc, live, mu, tab, two, g, t, [&](int j, int nt, uint32_t(&v)[4]) {
-            v[0] = v[1] = v[2] = v[3] = 0u;
-            if (!col[nt]) return;
-            const int64_t q = off[nt] + l * few::kStepK + few::x_chunk<F>(j, t) * 8;
-            if (!conv) {
-                const uint4 u = few::ld_global16(p.act16 + q);
-                v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-            } else {
+    };
+    auto mul = [&](const uint8_t* entry, int step) {
+        Ahead<NT> q;
+        constexpr int kW = Ahead<NT>::kWords;
+        const bool two = run.whole(w, step);
+        auto ahead = [&](int j) {
+            if (j % kW != 0) return;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 u = few::ld_global16(p.act32 + q + 4 * i);
-                    const __half2 lo = __floats2half2_rn(__uint_as_float(u.x) * fct[nt], __uint_as_float(u.y) * fct[nt]);
-                    const __half2 hi = __floats2half2_rn(__uint_as_float(u.z) * fct[nt], __uint_as_float(u.w) * fct[nt]);
-                    v[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
-                    v[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
-                }
-            }
+            for (int nt = 0; nt < NT; ++nt)
+                if (NT == 1 || (col.live >> nt & 1))
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) {
+                        if (F != few::kG128 && j + i >= 2 && !two) break;
+                        const int64_t o = off[nt] + step * few::kStepK + few::x_chunk<F>(j + i, t) * 8;
+                        if (!conv) {
+                            const uint4 u = few::ld_global16(p.act16 + o);
+                            q.v[nt][i][0] = u.x; q.v[nt][i][1] = u.y; q.v[nt][i][2] = u.z; q.v[nt][i][3] = u.w;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint4 u = few::ld_global16(p.act32 + o + 4 * k);
+                                const __half2 lo = __floats2half2_rn(__uint_as_float(u.x) * fct[nt], __uint_as_float(u.y) * fct[nt]);
+                                const __half2 hi = __floats2half2_rn(__uint_as_float(u.z) * fct[nt], __uint_as_float(u.w) * fct[nt]);
+                                q.v[nt][i][2 * k] = *reinterpret_cast<const uint32_t*>(&lo);
+                                q.v[nt][i][2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+                            }
+                        }
+                    }
+        };
+        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = q.v[nt][j % kW][i];
         });
     };
     auto finish = [&](int tile) {
+        const int r0 = (tile % row_tiles) * 16;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int tok = nt * 8 + 2 * t + c;
-                if (tok >= p.m) continue;
+                const int j = nt * 8 + 2 * t + c;
+                if (j >= col.cnt) continue;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = tile * 16 + 8 * i + g;
-                    if (r >= (g1 - g0) * 8) continue;
-                    // the factor is a power of two: so is its reciprocal
-                    const float v = conv ? acc[nt][2 * i + c] / factor[tok] : acc[nt][2 * i + c];
-                    if (p.splits > 1) part[tok * p.part_rows + r] = v;
-                    else p.y[static_cast<int64_t>(tok) * p.h + g0 * 8 + r] = __float2bfloat16_rn(v);
-                }
+                for (int i = 0; i < 2; ++i)
+                    if (r0 + 8 * i < (g1 - g0) * 8) part[(col.base + j) * p.part_rows + r0 + 8 * i + g] = run.acc[nt][2 * i + c];
             }
     };
-    if (ns > 0) {
-        few::run<kDepth, NT>(acc, reinterpret_cast<float4*>(smem + p.slots_at), warp, lane, runs, ns, next, [](int) {}, mul, finish);
-    } else {  // fewer steps than CTAs of the cluster: this one adds nothing
-        for (int i = threadIdx.x; i < p.m * p.part_rows; i += kThreads) part[i] = 0.0f;
-    }
-    if (p.splits == 1) return;
-    cluster_sync();
-    const uint32_t base = smem_u32(part);
+    run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, mul, finish);
+    __syncthreads();
     const int rows = (g1 - g0) * 8;
-    for (int i = threadIdx.x + rank * kThreads; i < p.m * rows; i += kThreads * p.splits) {
+    for (int i = threadIdx.x; i < p.m * rows; i += blockDim.x) {
         const int tok = i / rows, r = i - tok * rows;
         float v = 0.0f;
-        for (int s = 0; s < p.splits; ++s)
-            v += ld_shared_cluster_f32(map_shared_rank(base + (tok * p.part_rows + r) * 4, static_cast<uint32_t>(s)));
-        p.y[static_cast<int64_t>(tok) * p.h + g0 * 8 + r] = __float2bfloat16_rn(v);
+        for (int j = 0; j < p.top; ++j) v += part[R.pair[tok][j] * p.part_rows + r];
+        // the factor is a power of two: so is its reciprocal
+        p.y[static_cast<int64_t>(tok) * p.h + g0 * 8 + r] = __float2bfloat16_rn(conv ? v / factor[tok] : v);
     }
-    cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
 // ------------------------------- host side -------------------------------
@@ -562,7 +515,7 @@ static few::Weight weight_of(const MoeWeight& w) {
     o.absmax_scale = w.absmax_scale;
     o.mu = w.absmax_offset;
     o.codebook = w.codebook;
-    o.pairs = w.k % few::kStepK == 0 && reinterpret_cast<uintptr_t>(w.absmax_q) % 2 == 0;
+    o.units = static_cast<int>(w.k / few::kItemK);
     return o;
 }
 // Index of a kernel's instance for a weight: the table form, then three group sizes with and without zero points.
@@ -605,8 +558,7 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
      reinterpret_cast<const void*>(&K<few::kG128, true, __VA_ARGS__>),   reinterpret_cast<const void*>(&K<few::kG64, false, __VA_ARGS__>),  \
      reinterpret_cast<const void*>(&K<few::kG64, true, __VA_ARGS__>),    reinterpret_cast<const void*>(&K<few::kG32, false, __VA_ARGS__>),  \
      reinterpret_cast<const void*>(&K<few::kG32, true, __VA_ARGS__>)}
-    static const void* const up_fns[3][7] = {NF4_MOE_FORMS(k_moe_gate_up, 1, true), NF4_MOE_FORMS(k_moe_gate_up, 2, true),
-                                             NF4_MOE_FORMS(k_moe_gate_up, 2, false)};
+    static const void* const up_fns[2][7] = {NF4_MOE_FORMS(k_moe_gate_up, 1), NF4_MOE_FORMS(k_moe_gate_up, 2)};
     static const void* const down_fns[2][7] = {NF4_MOE_FORMS(k_moe_down, 1), NF4_MOE_FORMS(k_moe_down, 2)};
 #undef NF4_MOE_FORMS
     for (int64_t t = 0; t < m; t += kMaxM) {
@@ -622,32 +574,31 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
 
         int fit = 0;
         const int nt = p.m > 8 ? 2 : 1;
-        const int ring = kWarps * kDepth * few::kStepBytes, sums = kWarps * nt * 512;
-        p.ring_at = gate_up.integer ? 0 : few::kTableBytes;
-        p.slots_at = p.ring_at + ring;
-        p.x_at = p.slots_at + sums;
-        p.x_stride = static_cast<int>((h + few::kStepK - 1) / few::kStepK * few::kStepK * 2) + (gate_up.integer && gate_up.int4.group == 32 ? 64 : 16);
-        const bool on_chip = p.x_at + static_cast<size_t>(p.m) * p.x_stride <= few::kMaxSmem;
-        const void* fn = up_fns[on_chip ? nt - 1 : 2][form_of(gate_up)];
-        // the form without X on chip is made for two n-tiles alone
-        size_t smem = on_chip ? p.x_at + static_cast<size_t>(p.m) * p.x_stride : p.slots_at + kWarps * 2 * 512;
-        if ((e = few::resident(fn, kThreads, 1, dev, &fit)) != cudaSuccess) return e;
-        const int64_t most = (E < p.m * top ? E : p.m * top) * (f / 8);
-        if ((e = few::launch(fn, most < fit ? most : fit, kThreads, smem, 1, stream, args)) != cudaSuccess) return e;
+        const int64_t chosen = E < p.m * top ? E : p.m * top;  // at most
+        auto warps_of = [&](int64_t steps) { return steps <= few::kFewSteps ? few::kFewWarps : few::kMaxWarps; };
+        auto arrange = [&](const MoeWeight& w, int warps) {
+            p.ring_at = w.integer ? 0 : few::kTableBytes;
+            p.slots_at = p.ring_at + warps * kDepth * few::kStepBytes;
+            p.part_at = p.slots_at + warps * nt * 512;
+        };
+        const void* fn = up_fns[nt - 1][form_of(gate_up)];
+        if ((e = few::resident(fn, 1, dev, &fit)) != cudaSuccess) return e;
+        int64_t grid = chosen * (f / 8) < fit ? chosen * (f / 8) : fit;
+        int warps = warps_of((chosen * (f / 8) + grid - 1) / grid * ((h + few::kStepK - 1) / few::kStepK));
+        arrange(gate_up, warps);
+        if ((e = few::launch(fn, grid, warps * 32, p.part_at, 1, stream, args)) != cudaSuccess) return e;
 
-        // down: clusters of four where their rows come out even over the SMs
+        // down: so many output rows a CTA that the pairs' products fit
         fn = down_fns[nt - 1][form_of(down)];
-        p.splits = 4;
-        if ((e = few::resident(fn, kThreads, p.splits, dev, &fit)) != cudaSuccess) return e;
-        const int clusters = static_cast<int>(h / 8 < fit ? h / 8 : fit);
-        p.rows = few::shares_of(static_cast<int>(h / 8), clusters);
-        p.part_rows = static_cast<int>((h / 8 + clusters - 1) / clusters * 8);
-        p.ring_at = down.integer ? 0 : few::kTableBytes;
-        p.slots_at = p.ring_at + ring;
-        p.part_at = p.slots_at + sums;
-        smem = p.part_at + static_cast<size_t>(p.m) * p.part_rows * 4;
-        if (smem > few::kMaxSmem) return cudaErrorInvalidConfiguration;
-        if ((e = few::launch(fn, static_cast<int64_t>(clusters) * p.splits, kThreads, smem, p.splits, stream, args)) != cudaSuccess) return e;
+        if ((e = few::resident(fn, 1, dev, &fit)) != cudaSuccess) return e;
+        grid = h / 8 < fit ? h / 8 : fit;
+        warps = warps_of(((h / 8 + grid - 1) / grid + 1) / 2 * chosen * ((f + few::kStepK - 1) / few::kStepK));
+        arrange(down, warps);
+        const int64_t pairs = p.m * top, room = few::kMaxSmem - p.part_at;
+        while ((h / 8 + grid - 1) / grid * 8 * pairs * 4 > room) grid += fit;
+        p.rows = few::shares_of(static_cast<int>(h / 8), static_cast<int>(grid));
+        p.part_rows = static_cast<int>((h / 8 + grid - 1) / grid * 8);
+        if ((e = few::launch(fn, grid, warps * 32, p.part_at + pairs * p.part_rows * 4, 1, stream, args)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -96,7 +96,7 @@ def _struct(**kw):
 
 
 BAD_STRUCTS = [({"magic": 1}, -5), ({"version": 2}, -5), ({"scale_dtype": 2}, -5), ({"reserved": 1}, -5), ({"wq": None}, -1),
-               ({"scale": None}, -1), ({"n": 0}, -2), ({"n": 1 << 31}, -2), ({"k": 96, "group": 32}, -2), ({"k": 65536 + 64}, -2),
+               ({"scale": None}, -1), ({"n": 0}, -2), ({"n": 1 << 30}, -2), ({"k": 96, "group": 32}, -2), ({"k": 65536 + 64}, -2),
                ({"group": 16}, -2), ({"group": 0}, -2), ({"group": -64}, -2), ({"group": 96, "k": 192}, -2),
                ({"group": 512}, -2), ({"wq": FAKE + 8}, -3), ({"scale": FAKE + 1}, -3), ({"scale": FAKE + 2, "scale_dtype": 0}, -3)]
 
