@@ -231,13 +231,16 @@ __device__ __forceinline__ uint32_t ring_place(int r, int c) {
 // second half of it stays unused), so that a byte in bits 8 .. 15 is an address as it is.
 constexpr int kTableBytes = 256 * 256;
 __device__ __forceinline__ void build_table(uint8_t* tab, int codebook) {
-    for (int i = threadIdx.x; i < 256 * 8; i += blockDim.x) {
+    // a lane holds one level; the two of a byte come by shuffles, and go to 16 bytes of its entry
+    const float mine = kCodebook[codebook][threadIdx.x & 15];
+    for (int i = threadIdx.x; i < 256 * 8; i += blockDim.x) {  // whole warps
         const int v = i >> 3;
-        const __half2 e = __floats2half2_rn(kCodebook[codebook][v >> 4], kCodebook[codebook][v & 15]);
+        const __half2 e = __floats2half2_rn(__shfl_sync(kFull, mine, v >> 4), __shfl_sync(kFull, mine, v & 15));
         const uint32_t u = *reinterpret_cast<const uint32_t*>(&e);
         *reinterpret_cast<uint4*>(tab + 256 * v + 16 * (i & 7)) = make_uint4(u, u, u, u);
     }
 }
+
 // The four words of a lane's row g (entry + 512: row g + 8) from a ring entry; `at`: the lane's
 // offsets in it.
 struct Places {
@@ -424,7 +427,14 @@ struct Shares {
     int each, more;
     __device__ __forceinline__ int start(int i) const { return i * each + min(i, more); }
 };
-__host__ __device__ inline Shares shares_of(int total, int parts) { return Shares{total / parts, total % parts}; }
+__host__ __device__ inline Shares shares_of(int total, int parts) {
+    const int each = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(parts));
+    return Shares{each, total - each * parts};
+}
+// Over the warps of a CTA, of which there are two numbers: no division by a variable.
+__device__ __forceinline__ Shares shares_of_warps(int total) {
+    return blockDim.x == kFewWarps * 32 ? shares_of(total, kFewWarps) : shares_of(total, kMaxWarps);
+}
 
 // ------------------------------ runs of steps ------------------------------
 // The steps of a CTA's tiles, one tile's after the other's, are cut into equal runs for
@@ -449,10 +459,7 @@ struct Runner {
     const uint8_t* c[2];  // the lane's first chunk of the rows of that tile
     int wtile, window;    // the next window
 
-    template <typename Rows>
-    __device__ __forceinline__ void aim_codes(const Weight& w, Rows&& rows) {
-        int64_t row[2];
-        rows(tile, row);
+    __device__ __forceinline__ void aim_codes(const Weight& w, const int64_t (&row)[2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) c[i] = w.wq + row[i] * (w.k >> 1) + 16 * t;
     }
@@ -472,7 +479,11 @@ struct Runner {
             if (++step == s0 + ns) {
                 step = s0;
                 ++tile;
-                if (sent < i1) aim_codes(w, rows);
+                if (sent < i1) {
+                    int64_t row[2];
+                    rows(tile, row);
+                    aim_codes(w, row);
+                }
             }
         }
         copies_commit();
@@ -508,9 +519,9 @@ struct Runner {
         step = s0 + i0 - tile * ns;
         window = step / kR;
         if (i0 < i1) {
-            aim_codes(w, rows);
             int64_t row[2];
             rows(tile, row);
+            aim_codes(w, row);
             side.aim(w, row);
         }
 #pragma unroll

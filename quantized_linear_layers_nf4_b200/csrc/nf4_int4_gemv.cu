@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
     const int g0 = a.rows.start(cl), g1 = a.rows.start(cl + 1);
     const int s0 = a.ks.start(rank), ns = a.ks.start(rank + 1) - s0;  // steps of a tile
     const int warps = blockDim.x >> 5;
-    const few::Shares runs = few::shares_of((g1 - g0 + 1) / 2 * ns, warps);
+    const few::Shares runs = few::shares_of_warps((g1 - g0 + 1) / 2 * ns);
     auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int grp = g0 + tile * 2;
         // where a run's last tile has one group, that takes the place of another CTA's, and rows

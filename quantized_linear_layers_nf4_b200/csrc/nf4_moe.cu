@@ -145,6 +145,7 @@ struct Route {
     uint16_t pair[kMaxM][kMaxTop];
     float pair_prob[kMaxPairs];
     uint8_t pair_tok[kMaxPairs];
+    uint32_t chunk[kMaxE / 32];
     int active;
 };
 
@@ -155,97 +156,114 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Every thread of the block; the logits are complete.  A warp per token finds the
-// top_k one after the other (the largest key by a warp reduction, among equal ones the
-// lowest index by another).
+__device__ __forceinline__ float key_value(uint32_t k) {  // and back; NaN for the key of NaN
+    return k == 1u ? __int_as_float(0x7fffffff) : __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
+// One token's choice, by a warp: C = ceil(E / 32) logits a lane; the largest key by a warp
+// reduction, among equal ones the lowest expert by another.  A lone warp's instructions follow
+// one another slowly, so there are few: the number of logits is a constant, and what can be
+// done for all choices at once is done after the loop.
+template <int C>
+__device__ __forceinline__ void choose(const Params& p, Route& R, int t, int lane) {
+    uint32_t key[C];
+    const float* l = p.logits + t * p.E;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = 32 * i + lane;
+        key[i] = e < p.E ? order_key(__ldcg(l + e)) : 0u;
+    }
+    uint32_t all[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) all[i] = key[i];
+    uint32_t mine = 0, best = 0;
+    int id = 0;
+    for (int j = 0; j < p.top; ++j) {
+        uint32_t k = key[0];
+#pragma unroll
+        for (int i = 1; i < C; ++i) k = max(k, key[i]);
+        k = __reduce_max_sync(kFull, k);
+        uint32_t at = 0xffffu;
+#pragma unroll
+        for (int i = C - 1; i >= 0; --i)
+            if (key[i] == k) at = 32 * i + lane;
+        at = __reduce_min_sync(kFull, at);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (at == 32u * i + lane) key[i] = 0;
+        if (j == 0) best = k;
+        if (lane == j) {
+            mine = k;
+            id = static_cast<int>(at);
+        }
+    }
+    const float top = key_value(best), ex = lane < p.top ? expf(key_value(mine) - top) : 0.0f;
+    float total = 0.0f;
+    if (p.renormalize) {
+        total = ex;
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) total += all[i] ? expf(key_value(all[i]) - top) : 0.0f;
+    }
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+    if (lane < p.top) {
+        R.id[t][lane] = static_cast<uint16_t>(id);
+        R.prob[t][lane] = ex / total;
+        atomicOr(&R.mask[id], 1u << t);
+    }
+}
+
+// Every thread of the block; the logits are complete.
 __device__ __forceinline__ void route(const Params& p, Route& R) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, warp = few::warp_index(), lane = tid & 31, warps = blockDim.x >> 5;
     for (int e = tid; e < p.E; e += blockDim.x) R.mask[e] = 0;
     __syncthreads();
     for (int t = warp; t < p.m; t += warps) {
-        float v[kMaxE / 32];
-        uint32_t key[kMaxE / 32];
-        const float* l = p.logits + t * p.E;
-#pragma unroll
-        for (int i = 0; i < kMaxE / 32; ++i) {
-            const int e = 32 * i + lane;
-            key[i] = 0;
-            v[i] = 0.0f;
-            if (32 * i < p.E && e < p.E) {
-                v[i] = __ldcg(l + e);
-                key[i] = order_key(v[i]);
-            }
-        }
-        float best = 0.0f, mine = 0.0f, chosen = 0.0f;
-        for (int j = 0; j < p.top; ++j) {
-            uint32_t k = 0;
-#pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i)
-                if (32 * i < p.E) k = max(k, key[i]);
-            const uint32_t kmax = __reduce_max_sync(kFull, k);
-            uint32_t at = 0xffffffffu;
-#pragma unroll
-            for (int i = kMaxE / 32 - 1; i >= 0; --i)
-                if (32 * i < p.E && key[i] == kmax) at = 32 * i + lane;
-            at = __reduce_min_sync(kFull, at);
-            float got = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i)
-                if (32 * i < p.E && 32 * i + lane == static_cast<int>(at)) {
-                    got = v[i];
-                    key[i] = 0;
-                }
-            got = __shfl_sync(kFull, got, at & 31);
-            if (j == 0) best = got;
-            const float ex = expf(got - best);
-            chosen += ex;
-            if (lane == j) mine = ex;
-            if (lane == 0) {
-                R.id[t][j] = static_cast<uint16_t>(at);
-                atomicOr(&R.mask[at], 1u << t);
-            }
-        }
-        if (!p.renormalize) {
-            chosen = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i)
-                if (32 * i + lane < p.E) chosen += expf(v[i] - best);
-            for (int o = 16; o > 0; o >>= 1) chosen += __shfl_xor_sync(kFull, chosen, o);
-        }
-        if (lane < p.top) R.prob[t][lane] = mine / chosen;
+        if (p.E <= 32) choose<1>(p, R, t, lane);
+        else if (p.E <= 64) choose<2>(p, R, t, lane);
+        else if (p.E <= 128) choose<4>(p, R, t, lane);
+        else if (p.E <= 256) choose<8>(p, R, t, lane);
+        else choose<16>(p, R, t, lane);
     }
     __syncthreads();
-    if (warp == 0) {
-        int n = 0, pairs = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int cnt = e < p.E ? __popc(R.mask[e]) : 0;
-            const uint32_t any = __ballot_sync(kFull, cnt != 0);
-            int sum = cnt;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(kFull, sum, o);
-                if (lane >= o) sum += up;
-            }
-            if (cnt) {
-                const int at = n + __popc(any & ((1u << lane) - 1));
-                R.list[at] = static_cast<uint16_t>(e);
-                R.base[at] = static_cast<uint16_t>(pairs + sum - cnt);
-                R.pos[e] = static_cast<uint16_t>(at);
-            }
-            n += __popc(any);
-            pairs += __shfl_sync(kFull, sum, 31);
+    // the list: a warp for each 32 experts counts its chosen ones and their pairs, then finds its place
+    const int chunks = (p.E + 31) >> 5;
+    for (int c = warp; c < chunks; c += warps) {
+        const int e = 32 * c + lane;
+        const int cnt = e < p.E ? __popc(R.mask[e]) : 0;
+        const uint32_t any = __ballot_sync(kFull, cnt != 0);
+        const int sum = __reduce_add_sync(kFull, cnt);
+        if (lane == 0) R.chunk[c] = static_cast<uint32_t>(__popc(any)) << 16 | sum;
+    }
+    __syncthreads();
+    for (int c = warp; c < chunks; c += warps) {
+        const int e = 32 * c + lane;
+        const int cnt = e < p.E ? __popc(R.mask[e]) : 0;
+        const uint32_t any = __ballot_sync(kFull, cnt != 0);
+        const uint32_t before = __reduce_add_sync(kFull, lane < c ? R.chunk[lane] : 0u);
+        int sum = cnt;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(kFull, sum, o);
+            if (lane >= o) sum += up;
         }
-        if (lane == 0) {
-            R.active = n;
-            R.base[n] = static_cast<uint16_t>(pairs);
+        if (cnt) {
+            const int at = static_cast<int>(before >> 16) + __popc(any & ((1u << lane) - 1));
+            R.list[at] = static_cast<uint16_t>(e);
+            R.base[at] = static_cast<uint16_t>((before & 0xffffu) + sum - cnt);
+            R.pos[e] = static_cast<uint16_t>(at);
+        }
+        if (c == chunks - 1 && lane == 31) {
+            R.active = static_cast<int>(before >> 16) + __popc(any);
+            R.base[R.active] = static_cast<uint16_t>((before & 0xffffu) + sum);
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.m * p.top; i += blockDim.x) {
-        const int t = i / p.top, j = i % p.top, e = R.id[t][j];
+    for (int t = warp; t < p.m; t += warps) {
+        if (lane >= p.top) continue;
+        const int e = R.id[t][lane];
         const int pair = R.base[R.pos[e]] + __popc(R.mask[e] & ((1u << t) - 1));
-        R.pair[t][j] = static_cast<uint16_t>(pair);
-        R.pair_prob[pair] = R.prob[t][j];
+        R.pair[t][lane] = static_cast<uint16_t>(pair);
+        R.pair_prob[pair] = R.prob[t][lane];
         R.pair_tok[pair] = static_cast<uint8_t>(t);
     }
     __syncthreads();
@@ -301,7 +319,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
     const few::Shares mine = few::shares_of(R.active * per_e, gridDim.x);
     const int t0 = mine.start(blockIdx.x), t1 = mine.start(blockIdx.x + 1);
     const int ns = (p.h + few::kStepK - 1) / few::kStepK;
-    const few::Shares runs = few::shares_of((t1 - t0) * ns, blockDim.x >> 5);
+    const few::Shares runs = few::shares_of_warps((t1 - t0) * ns);
 
     auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int idx = (t0 + tile) / per_e;
@@ -389,7 +407,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
     const int g0 = p.rows.start(blockIdx.x), g1 = p.rows.start(blockIdx.x + 1);
     const int row_tiles = (g1 - g0 + 1) / 2;
     const int ns = (p.f + few::kStepK - 1) / few::kStepK;
-    const few::Shares runs = few::shares_of(R.active * row_tiles * ns, blockDim.x >> 5);
+    const few::Shares runs = few::shares_of_warps(R.active * row_tiles * ns);
 
     auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int idx = tile / row_tiles, grp = g0 + (tile - idx * row_tiles) * 2;
