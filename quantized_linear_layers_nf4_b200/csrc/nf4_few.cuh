@@ -298,7 +298,7 @@ __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t*
     ring_words<F>(entry, at, c[0]);
     ring_words<F>(entry + 512, at, c[1]);
     constexpr int kR = window_steps<F>(), kU = 4 / kR;
-    const int unit = step % kR * kU;  // of the step's first group
+    const int unit = static_cast<int>(static_cast<unsigned>(step) % kR * kU);  // of the step's first group
     float p[NT][4], f[2] = {0.0f, 0.0f};
     uint32_t zz[2] = {0x00080008u, 0x00080008u};
 #pragma unroll
@@ -444,7 +444,9 @@ __device__ __forceinline__ Shares shares_of_warps(int total) {
 //   begin(tile)          as a tile is entered
 //   mul(entry, step)     multiplies a step of the tile, counted from the row's first
 //   finish(tile)         its sums are complete in acc
-template <int F, bool Z, int kDepth, int NT>
+// kFour: the inner loop takes four steps at a time where it can; without it the code and its
+// registers stay small enough for the mixture-of-experts kernels.
+template <int F, bool Z, int kDepth, int NT, bool kFour>
 struct Runner {
     static constexpr int kR = window_steps<F>();
     Sides<F, Z> side;
@@ -466,25 +468,32 @@ struct Runner {
     __device__ __forceinline__ bool whole(const Weight& w, int st) const {  // a step's second half is not past the end of k
         return F == kG128 || (st + 1) * kStepK <= w.k;
     }
+    __device__ __forceinline__ void copy(uint32_t entry, uint64_t to, bool two) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (F == kG128) copy16(put + entry + 512 * i, c[i] + to);
+            else copy16(put + entry + 512 * i, c[i] + to, two || t < 2 ? 16 : 0);
+        }
+    }
+    template <typename Rows>
+    __device__ __forceinline__ void moved(const Weight& w, int n, Rows&& rows) {  // n steps were sent
+        sent += n;
+        step += n;
+        if (step == s0 + ns) {
+            step = s0;
+            ++tile;
+            if (sent < i1) {
+                int64_t row[2];
+                rows(tile, row);
+                aim_codes(w, row);
+            }
+        }
+    }
     template <typename Rows>
     __device__ __forceinline__ void send(const Weight& w, uint32_t entry, Rows&& rows) {
         if (sent < i1) {
-            const uint64_t to = static_cast<uint64_t>(static_cast<uint32_t>(step) * (kStepK / 2u));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (F == kG128) copy16(put + entry + 512 * i, c[i] + to);
-                else copy16(put + entry + 512 * i, c[i] + to, whole(w, step) || t < 2 ? 16 : 0);
-            }
-            ++sent;
-            if (++step == s0 + ns) {
-                step = s0;
-                ++tile;
-                if (sent < i1) {
-                    int64_t row[2];
-                    rows(tile, row);
-                    aim_codes(w, row);
-                }
-            }
+            copy(entry, static_cast<uint32_t>(step) * (kStepK / 2u), whole(w, step));
+            moved(w, 1, rows);
         }
         copies_commit();
     }
@@ -501,9 +510,9 @@ struct Runner {
             side.aim(w, row);
         }
     }
-    // Starts the first loads of the run.
+    // Finds the run; reads nothing of the weight.
     template <typename Rows>
-    __device__ __forceinline__ void start(const Weight& w, uint8_t* rings, int warp_, int lane_, const Shares& runs, int s0_, int ns_,
+    __device__ __forceinline__ void find(const Weight& w, uint8_t* rings, int warp_, int lane_, const Shares& runs, int s0_, int ns_,
                                           Rows&& rows) {
         warp = warp_;
         lane = lane_;
@@ -524,6 +533,10 @@ struct Runner {
             aim_codes(w, row);
             side.aim(w, row);
         }
+    }
+    // Starts its first loads.
+    template <typename Rows>
+    __device__ __forceinline__ void start(const Weight& w, Rows&& rows) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) send(w, d * kStepBytes, rows);
         if (i0 < i1) next_window(w, rows);
@@ -545,21 +558,50 @@ struct Runner {
             begin(tl);
             const int n = min(ns - st, i1 - i);
             i += n;
-            side.turn(w, mu);
-            next_window(w, rows);
             st += s0;
-            for (const int end = st + n;;) {
+            auto turn = [&] {
+                side.turn(w, mu);
+                next_window(w, rows);
+            };
+            auto wrap = [&] { entry = entry == (kDepth - 1) * kStepBytes ? 0u : entry + kStepBytes; };
+            auto ready = [&] {
                 copies_wait<kDepth - 1>();
                 if (F != kG128) __syncwarp();  // else a lane reads what it copied itself
-                mul(ring + entry, st);
-                if (F != kG128) __syncwarp();
-                send(w, entry, rows);
-                entry = entry == (kDepth - 1) * kStepBytes ? 0u : entry + kStepBytes;
-                if (++st == end) break;
-                if (st % kR == 0) {
-                    side.turn(w, mu);
-                    next_window(w, rows);
+            };
+            turn();
+            for (const int end = st + n;;) {
+                if (kFour && (st & 3) == 0 && st + 4 <= end) {
+                    // four steps from a multiple of four on: windows and offsets are constants, and
+                    // as a rule the four that follow are one more piece of the same rows
+                    const unsigned q = static_cast<unsigned>(st) >> 2;
+                    const bool plain = sent + 4 <= i1 && step + 4 <= s0 + ns && whole(w, step + 3);
+                    const uint32_t to = static_cast<uint32_t>(step) * (kStepK / 2u);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (s > 0 && s % kR == 0) turn();
+                        ready();
+                        mul(ring + entry, static_cast<int>(4 * q + s));
+                        if (F != kG128) __syncwarp();
+                        if (plain) {
+                            copy(entry, to + s * (kStepK / 2u), true);
+                            copies_commit();
+                        } else {
+                            send(w, entry, rows);
+                        }
+                        wrap();
+                    }
+                    if (plain) moved(w, 4, rows);
+                    st += 4;
+                } else {
+                    ready();
+                    mul(ring + entry, st);
+                    if (F != kG128) __syncwarp();
+                    send(w, entry, rows);
+                    wrap();
+                    ++st;
                 }
+                if (st == end) break;
+                if (st % kR == 0) turn();
             }
             st -= s0;
             if (st < ns) break;

@@ -56,9 +56,10 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
         row[0] = min(static_cast<int64_t>(grp) * 8 + g, a.w.n - 1);
         row[1] = grp + 1 < g1 ? min(static_cast<int64_t>(grp) * 8 + 8 + g, a.w.n - 1) : row[0];
     };
-    few::Runner<F, Z, depth_of(NT), NT> R;
+    few::Runner<F, Z, depth_of(NT), NT, true> R;
+    R.find(a.w, smem + a.ring_at, warp, lane, runs, s0, ns, rows_of);
     if (!a.early) grid_dependency_wait();
-    R.start(a.w, smem + a.ring_at, warp, lane, runs, s0, ns, rows_of);
+    R.start(a.w, rows_of);
     if (a.early) grid_dependency_wait();
     grid_launch_dependents();
     // this CTA's k range of X

@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
         row[0] = static_cast<int64_t>(R.list[idx]) * 2 * p.f + (t0 + tile - idx * per_e) * 8 + g;
         row[1] = row[0] + p.f;
     };
-    few::Runner<F, Z, kDepth, NT> run;
-    run.start(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
+    few::Runner<F, Z, kDepth, NT, false> run;
+    run.find(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
+    run.start(w, rows_of);
 
     Columns<NT> col;
     const __half* x[NT];
@@ -415,8 +416,9 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
         // where the second half is another CTA's, the first takes its place and is not stored
         row[1] = row[0] + (grp + 1 < g1 ? 8 : 0);
     };
-    few::Runner<F, Z, kDepth, NT> run;
-    run.start(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
+    few::Runner<F, Z, kDepth, NT, false> run;
+    run.find(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
+    run.start(w, rows_of);
     grid_dependency_wait();
     grid_launch_dependents();
 
