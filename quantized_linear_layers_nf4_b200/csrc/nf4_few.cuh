@@ -169,7 +169,8 @@ template <int F, bool Z>
 struct Sides {
     const uint8_t* s[2];  // of the rows' first group; absmax codes
     const uint8_t* z[2];
-    int64_t e[2];         // kTable: index of the rows' first absmax code
+    const float* e[2];    // kTable: scale of the rows' first absmax code, and that code's place under it
+    uint32_t at[2];
     uint32_t raw_s[2], raw_z[2];  // of the next window, as loaded: anything done to it would wait for it
     float f[2];           // of this window
     uint32_t zz[2];       // zero points of this window, in both halves
@@ -178,8 +179,10 @@ struct Sides {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (F == kTable) {
-                e[i] = row[i] * (w.k / kItemK);
-                s[i] = reinterpret_cast<const uint8_t*>(w.absmax_q) + e[i];
+                const int64_t first = row[i] * w.units;
+                s[i] = reinterpret_cast<const uint8_t*>(w.absmax_q) + first;
+                e[i] = w.absmax_scale + (first >> 8);
+                at[i] = static_cast<uint32_t>(first) & 255u;
             } else {
                 s[i] = reinterpret_cast<const uint8_t*>(w.scale) + (w.f32 ? 4 * row[i] : 2 * row[i]);
                 if (Z) z[i] = w.zero + row[i];
@@ -192,7 +195,7 @@ struct Sides {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 raw_z[i] = static_cast<uint32_t>(static_cast<int32_t>(__ldg(reinterpret_cast<const int8_t*>(s[i] + unit))));
-                raw_s[i] = __float_as_uint(__ldg(w.absmax_scale + ((e[i] + unit) >> 8)));
+                raw_s[i] = __float_as_uint(__ldg(e[i] + ((at[i] + unit) >> 8)));
             }
             return;
         }
@@ -228,7 +231,7 @@ __device__ __forceinline__ uint32_t ring_place(int r, int c) {
 }
 
 // The two levels of each byte value as fp16, one copy a bank, 256 bytes an entry (the
-// second half of it stays unused), so that a byte in bits 8 .. 15 is an address as it is.
+// second half of it stays unused), so that a byte above a bank's offset is an address.
 constexpr int kTableBytes = 256 * 256;
 __device__ __forceinline__ void build_table(uint8_t* tab, int codebook) {
     // a lane holds one level; the two of a byte come by shuffles, and go to 16 bytes of its entry
@@ -274,15 +277,16 @@ __device__ __forceinline__ void ring_words(const uint8_t* entry, const Places& a
     }
 }
 
-// A word as four fp16 pairs; zz: the zero point in both halves; tab: the lane's copy of the table.
+// A word as four fp16 pairs; zz: the zero point in both halves; tab: the table, bank: the lane's
+// copy of it (4 lane).
 template <int F>
-__device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* tab, uint32_t (&o)[4]) {
+__device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* tab, uint32_t bank, uint32_t (&o)[4]) {
     if (F == kTable) {
-        const uint32_t v = w >> 16;
-        o[0] = *reinterpret_cast<const uint32_t*>(tab + (w & 0xffu) * 256u);
-        o[1] = *reinterpret_cast<const uint32_t*>(tab + (w & 0xff00u));
-        o[2] = *reinterpret_cast<const uint32_t*>(tab + (v & 0xffu) * 256u);
-        o[3] = *reinterpret_cast<const uint32_t*>(tab + (v & 0xff00u));
+        // byte j of the word above the bank (under 128): the entry's offset by one permute
+        o[0] = *reinterpret_cast<const uint32_t*>(tab + prmt(w, bank, 0x5504));
+        o[1] = *reinterpret_cast<const uint32_t*>(tab + prmt(w, bank, 0x5514));
+        o[2] = *reinterpret_cast<const uint32_t*>(tab + prmt(w, bank, 0x5524));
+        o[3] = *reinterpret_cast<const uint32_t*>(tab + prmt(w, bank, 0x5534));
     } else {
         int4_f16(w, zlo_f16(zz), zhi_f16(zz), o);
     }
@@ -293,7 +297,7 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* t
 // ahead(j) comes before the first use of word j.  `step`: counted from the row's first.
 template <int F, bool Z, int NT, typename AF, typename XF>
 __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t* entry, const Places& at, float (&acc)[NT][4], int live,
-                                         const uint8_t* tab, int step, bool two, AF&& ahead, XF&& x) {
+                                         const uint8_t* tab, uint32_t bank, int step, bool two, AF&& ahead, XF&& x) {
     uint32_t c[2][4];
     ring_words<F>(entry, at, c[0]);
     ring_words<F>(entry + 512, at, c[1]);
@@ -315,8 +319,8 @@ __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t*
             }
         }
         uint32_t a[4], b[4];
-        decode<F>(c[0][j], zz[0], tab, a);
-        decode<F>(c[1][j], zz[1], tab, b);
+        decode<F>(c[0][j], zz[0], tab, bank, a);
+        decode<F>(c[1][j], zz[1], tab, bank, b);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (NT > 1 && !(live >> nt & 1)) continue;

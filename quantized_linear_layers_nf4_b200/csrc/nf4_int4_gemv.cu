@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
     }
     auto mul = [&](const uint8_t* entry, int step) {
         const uint32_t x0 = (step - s0) * (few::kStepK * 2);
-        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, 3, nullptr, step, R.whole(a.w, step), [](int) {}, [&](int j, int nt, uint32_t(&v)[4]) {
+        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, 3, nullptr, 0u, step, R.whole(a.w, step), [](int) {}, [&](int j, int nt, uint32_t(&v)[4]) {
             const uint4 u = *reinterpret_cast<const uint4*>(xb[nt][j >> 1] + x0 + few::x_word<F>(j));
             v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
         });

@@ -295,6 +295,17 @@ struct Ahead {
     uint32_t v[NT][kWords][4];
 };
 
+// Words j .. j + kW - 1 of a lane's X, `x` its first chunk of the step.
+template <int F, int kW>
+__device__ __forceinline__ void load_x(uint32_t (&v)[kW][4], const __half* x, int j, bool two) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+        if (F != few::kG128 && j + i >= 2 && !two) break;
+        const uint4 u = few::ld_global16(x + (few::x_chunk<F>(j + i, 0) - few::x_chunk<F>(0, 0)) * 8);
+        v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
+    }
+}
+
 // ------------------------------ gate and up ------------------------------
 template <int F, bool Z, int NT>
 __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __grid_constant__ Params p) {
@@ -314,7 +325,8 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
 
     const few::Weight& w = p.gate_up;
     const float mu = F == few::kTable ? __ldg(w.mu) : 0.0f;
-    const uint8_t* tab = smem + 4 * lane;
+    const uint8_t* tab = smem;
+    const uint32_t bank = 4 * lane;
     const int per_e = p.f / 8;
     const few::Shares mine = few::shares_of(R.active * per_e, gridDim.x);
     const int t0 = mine.start(blockIdx.x), t1 = mine.start(blockIdx.x + 1);
@@ -331,29 +343,24 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
     run.start(w, rows_of);
 
     Columns<NT> col;
-    const __half* x[NT];
+    const __half* x[NT];  // a lane's first chunk of its columns
     auto begin = [&](int tile) {
         if (!col.enter(R, (t0 + tile) / per_e, g)) return;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt] = p.xs + static_cast<int64_t>(R.pair_tok[col.pair[nt]]) * p.h;
+        for (int nt = 0; nt < NT; ++nt) x[nt] = p.xs + static_cast<int64_t>(R.pair_tok[col.pair[nt]]) * p.h + few::x_chunk<F>(0, t) * 8;
     };
     auto mul = [&](const uint8_t* entry, int step) {
         Ahead<NT> q;
         constexpr int kW = Ahead<NT>::kWords;
         const bool two = run.whole(w, step);
+        const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
         auto ahead = [&](int j) {
             if (j % kW != 0) return;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                if (NT == 1 || (col.live >> nt & 1))
-#pragma unroll
-                    for (int i = 0; i < kW; ++i) {
-                        if (F != few::kG128 && j + i >= 2 && !two) break;
-                        const uint4 u = few::ld_global16(x[nt] + step * few::kStepK + few::x_chunk<F>(j + i, t) * 8);
-                        q.v[nt][i][0] = u.x; q.v[nt][i][1] = u.y; q.v[nt][i][2] = u.z; q.v[nt][i][3] = u.w;
-                    }
+                if (NT == 1 || (col.live >> nt & 1)) load_x<F, kW>(q.v[nt], x[nt] + to, j, two);
         };
-        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
+        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, bank, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = q.v[nt][j % kW][i];
         });
@@ -386,6 +393,23 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
 }
 
 // --------------------------------- down ---------------------------------
+// As load_x, from fp32 and times a token's power of two.
+template <int F, int kW>
+__device__ __forceinline__ void load_wide(uint32_t (&v)[kW][4], const float* x, float up, int j, bool two) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+        if (F != few::kG128 && j + i >= 2 && !two) break;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 u = few::ld_global16(x + (few::x_chunk<F>(j + i, 0) - few::x_chunk<F>(0, 0)) * 8 + 4 * k);
+            const __half2 lo = __floats2half2_rn(__uint_as_float(u.x) * up, __uint_as_float(u.y) * up);
+            const __half2 hi = __floats2half2_rn(__uint_as_float(u.z) * up, __uint_as_float(u.w) * up);
+            v[i][2 * k] = *reinterpret_cast<const uint32_t*>(&lo);
+            v[i][2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+        }
+    }
+}
+
 // A CTA has a run of output rows; a tile is 16 of them with one chosen expert's f, its columns that
 // expert's pairs.  The products of a pair go to shared memory, and a token's are added there in the
 // order of its choices.
@@ -404,7 +428,8 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
 
     const few::Weight& w = p.down;
     const float mu = F == few::kTable ? __ldg(w.mu) : 0.0f;
-    const uint8_t* tab = smem + 4 * lane;
+    const uint8_t* tab = smem;
+    const uint32_t bank = 4 * lane;
     const int g0 = p.rows.start(blockIdx.x), g1 = p.rows.start(blockIdx.x + 1);
     const int row_tiles = (g1 - g0 + 1) / 2;
     const int ns = (p.f + few::kStepK - 1) / few::kStepK;
@@ -434,45 +459,27 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
     const bool conv = wide != 0;
 
     Columns<NT> col;
-    int64_t off[NT];
-    float fct[NT];
+    const __half* x[NT];  // a lane's first chunk of its columns
     auto begin = [&](int tile) {
         if (!col.enter(R, tile / row_tiles, g)) return;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            off[nt] = static_cast<int64_t>(col.pair[nt]) * p.f;
-            fct[nt] = factor[R.pair_tok[col.pair[nt]]];
-        }
+        for (int nt = 0; nt < NT; ++nt) x[nt] = p.act16 + static_cast<int64_t>(col.pair[nt]) * p.f + few::x_chunk<F>(0, t) * 8;
     };
     auto mul = [&](const uint8_t* entry, int step) {
         Ahead<NT> q;
         constexpr int kW = Ahead<NT>::kWords;
         const bool two = run.whole(w, step);
+        const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
         auto ahead = [&](int j) {
             if (j % kW != 0) return;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (NT == 1 || (col.live >> nt & 1))
-#pragma unroll
-                    for (int i = 0; i < kW; ++i) {
-                        if (F != few::kG128 && j + i >= 2 && !two) break;
-                        const int64_t o = off[nt] + step * few::kStepK + few::x_chunk<F>(j + i, t) * 8;
-                        if (!conv) {
-                            const uint4 u = few::ld_global16(p.act16 + o);
-                            q.v[nt][i][0] = u.x; q.v[nt][i][1] = u.y; q.v[nt][i][2] = u.z; q.v[nt][i][3] = u.w;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint4 u = few::ld_global16(p.act32 + o + 4 * k);
-                                const __half2 lo = __floats2half2_rn(__uint_as_float(u.x) * fct[nt], __uint_as_float(u.y) * fct[nt]);
-                                const __half2 hi = __floats2half2_rn(__uint_as_float(u.z) * fct[nt], __uint_as_float(u.w) * fct[nt]);
-                                q.v[nt][i][2 * k] = *reinterpret_cast<const uint32_t*>(&lo);
-                                q.v[nt][i][2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hi);
-                            }
-                        }
-                    }
+            for (int nt = 0; nt < NT; ++nt) {
+                if (NT > 1 && !(col.live >> nt & 1)) continue;
+                if (!conv) load_x<F, kW>(q.v[nt], x[nt] + to, j, two);
+                else load_wide<F, kW>(q.v[nt], p.act32 + (x[nt] - p.act16) + to, factor[R.pair_tok[col.pair[nt]]], j, two);
+            }
         };
-        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
+        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, bank, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = q.v[nt][j % kW][i];
         });
