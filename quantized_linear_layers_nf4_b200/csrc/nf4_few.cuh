@@ -293,11 +293,10 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* t
 }
 
 // acc += (16 rows x 128 k of W) x (128 k x 8 NT columns of X); x(j, nt, v) gives the lane's
-// eight values of word j, column g of n-tile nt; n-tiles without a bit in `live` are left out;
-// ahead(j) comes before the first use of word j.  `step`: counted from the row's first.
-template <int F, bool Z, int NT, typename AF, typename XF>
-__device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t* entry, const Places& at, float (&acc)[NT][4], int live,
-                                         const uint8_t* tab, uint32_t bank, int step, bool two, AF&& ahead, XF&& x) {
+// eight values of word j, column g of n-tile nt.  `step`: counted from the row's first.
+template <int F, bool Z, int NT, typename XF>
+__device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t* entry, const Places& at, float (&acc)[NT][4],
+                                         const uint8_t* tab, uint32_t bank, int step, bool two, XF&& x) {
     uint32_t c[2][4];
     ring_words<F>(entry, at, c[0]);
     ring_words<F>(entry + 512, at, c[1]);
@@ -308,7 +307,6 @@ __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t*
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (F != kG128 && j == 2 && !two) return;
-        ahead(j);
         const bool first = F == kG128 ? j == 0 : (F == kG32 || (j & 1) == 0);
         const bool last = F == kG128 ? j == 3 : (F == kG32 || (j & 1) == 1);
         if (first) {
@@ -323,7 +321,6 @@ __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t*
         decode<F>(c[1][j], zz[1], tab, bank, b);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && !(live >> nt & 1)) continue;
             uint32_t v[4];
             x(j, nt, v);
             if (first) mma_f16_first(p[nt], a[0], b[0], a[1], b[1], v[0], v[1]);
@@ -333,8 +330,7 @@ __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t*
         if (last) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                if (NT > 1 && !(live >> nt & 1)) continue;
-                acc[nt][0] = __fmaf_rn(f[0], p[nt][0], acc[nt][0]);
+                    acc[nt][0] = __fmaf_rn(f[0], p[nt][0], acc[nt][0]);
                 acc[nt][1] = __fmaf_rn(f[0], p[nt][1], acc[nt][1]);
                 acc[nt][2] = __fmaf_rn(f[1], p[nt][2], acc[nt][2]);
                 acc[nt][3] = __fmaf_rn(f[1], p[nt][3], acc[nt][3]);

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
     }
     auto mul = [&](const uint8_t* entry, int step) {
         const uint32_t x0 = (step - s0) * (few::kStepK * 2);
-        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, 3, nullptr, 0u, step, R.whole(a.w, step), [](int) {}, [&](int j, int nt, uint32_t(&v)[4]) {
+        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, nullptr, 0u, step, R.whole(a.w, step), [&](int j, int nt, uint32_t(&v)[4]) {
             const uint4 u = *reinterpret_cast<const uint4*>(xb[nt][j >> 1] + x0 + few::x_word<F>(j));
             v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
         });
@@ -159,7 +159,7 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     if (e != cudaSuccess) return e;
     int64_t clusters = fit < groups ? fit : groups;
     const int64_t steps = ((groups + clusters - 1) / clusters + 1) / 2 * ((all + splits - 1) / splits);
-    const int warps = steps <= few::kFewSteps && m <= few::kFewWarps ? few::kFewWarps : few::kMaxWarps;  // a warp or more a token for X
+    const int warps = steps <= (m > 4 ? 1 : 2) * few::kFewSteps && m <= few::kFewWarps ? few::kFewWarps : few::kMaxWarps;  // a warp or more a token for X
     const Room at = room_of(m, w.k, splits, fmt, warps);
     if (at.left < m * 64) return cudaErrorInvalidConfiguration;
     while (splits > 1 && (groups + clusters - 1) / clusters * 8 * m * 4 > at.left) clusters += fit;

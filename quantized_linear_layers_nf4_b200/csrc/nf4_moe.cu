@@ -137,9 +137,9 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const __grid_cons
 // ------------------------------- routing -------------------------------
 struct Route {
     uint32_t mask[kMaxE];         // tokens of an expert
-    uint16_t pos[kMaxE];          // of an expert in the list of chosen ones
-    uint16_t list[kMaxPairs];     // chosen experts, ascending
-    uint16_t base[kMaxPairs + 1]; // first pair of a chosen expert; the pairs of an expert are by token
+    uint16_t pos[kMaxE];          // of an expert's first entry in the list
+    uint16_t list[kMaxPairs];     // chosen experts, ascending, once for each eight of their tokens
+    uint16_t base[kMaxPairs + 1]; // first pair of an entry; the pairs of an expert are by token
     float prob[kMaxM][kMaxTop];
     uint16_t id[kMaxM][kMaxTop];
     uint16_t pair[kMaxM][kMaxTop];
@@ -226,35 +226,37 @@ __device__ __forceinline__ void route(const Params& p, Route& R) {
         else choose<16>(p, R, t, lane);
     }
     __syncthreads();
-    // the list: a warp for each 32 experts counts its chosen ones and their pairs, then finds its place
+    // the list: a warp for each 32 experts counts its entries and their pairs, then finds its place
     const int chunks = (p.E + 31) >> 5;
     for (int c = warp; c < chunks; c += warps) {
         const int e = 32 * c + lane;
         const int cnt = e < p.E ? __popc(R.mask[e]) : 0;
-        const uint32_t any = __ballot_sync(kFull, cnt != 0);
-        const int sum = __reduce_add_sync(kFull, cnt);
-        if (lane == 0) R.chunk[c] = static_cast<uint32_t>(__popc(any)) << 16 | sum;
+        const uint32_t both = __reduce_add_sync(kFull, static_cast<uint32_t>((cnt + 7) >> 3) << 16 | cnt);
+        if (lane == 0) R.chunk[c] = both;
     }
     __syncthreads();
     for (int c = warp; c < chunks; c += warps) {
         const int e = 32 * c + lane;
         const int cnt = e < p.E ? __popc(R.mask[e]) : 0;
-        const uint32_t any = __ballot_sync(kFull, cnt != 0);
         const uint32_t before = __reduce_add_sync(kFull, lane < c ? R.chunk[lane] : 0u);
-        int sum = cnt;
+        const uint32_t own = static_cast<uint32_t>((cnt + 7) >> 3) << 16 | cnt;
+        uint32_t sum = own;
         for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(kFull, sum, o);
+            const uint32_t up = __shfl_up_sync(kFull, sum, o);
             if (lane >= o) sum += up;
         }
+        const uint32_t first = before + sum - own;
         if (cnt) {
-            const int at = static_cast<int>(before >> 16) + __popc(any & ((1u << lane) - 1));
-            R.list[at] = static_cast<uint16_t>(e);
-            R.base[at] = static_cast<uint16_t>((before & 0xffffu) + sum - cnt);
+            const int at = static_cast<int>(first >> 16);
             R.pos[e] = static_cast<uint16_t>(at);
+            for (int i = 0; 8 * i < cnt; ++i) {
+                R.list[at + i] = static_cast<uint16_t>(e);
+                R.base[at + i] = static_cast<uint16_t>((first & 0xffffu) + 8 * i);
+            }
         }
         if (c == chunks - 1 && lane == 31) {
-            R.active = static_cast<int>(before >> 16) + __popc(any);
-            R.base[R.active] = static_cast<uint16_t>((before & 0xffffu) + sum);
+            R.active = static_cast<int>((before + sum) >> 16);
+            R.base[R.active] = static_cast<uint16_t>(before + sum);
         }
     }
     __syncthreads();
@@ -269,45 +271,36 @@ __device__ __forceinline__ void route(const Params& p, Route& R) {
     __syncthreads();
 }
 
-// Columns of a chosen expert's products are its pairs (token, choice); those past them repeat the
-// last one, and are not used.
-template <int NT>
+// The eight columns of an entry's products are its pairs (token, choice); those past them repeat
+// the last one, and are not used.  An expert of more than eight tokens comes again for the
+// next eight: sums for sixteen at once cost registers and with them warps, on every call,
+// and few calls have such an expert.
 struct Columns {
-    int idx = -1, base = 0, cnt = 0, live = 0;  // expert of the list; its pairs; n-tiles with any
-    int pair[NT];                               // of the lane's columns
+    int idx = -1, base = 0, cnt = 0, pair = 0;  // entry of the list; its pairs; the lane's one
     __device__ __forceinline__ bool enter(const Route& R, int i, int g) {
         if (i == idx) return false;
         idx = i;
         base = R.base[i];
         cnt = R.base[i + 1] - base;
-        live = cnt > 8 ? 3 : 1;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) pair[nt] = base + min(nt * 8 + g, cnt - 1);
+        pair = base + min(g, cnt - 1);
         return true;
     }
 };
 
-// X of a step, from global memory through L1: with one n-tile all of it is asked for before
-// the first word is decoded, with two half of it.
-template <int NT>
-struct Ahead {
-    static constexpr int kWords = NT == 1 ? 4 : 2;
-    uint32_t v[NT][kWords][4];
-};
-
-// Words j .. j + kW - 1 of a lane's X, `x` its first chunk of the step.
-template <int F, int kW>
-__device__ __forceinline__ void load_x(uint32_t (&v)[kW][4], const __half* x, int j, bool two) {
+// A lane's X of a step, from global memory through L1, `x` its first chunk: all of it is asked
+// for before the first word is decoded.
+template <int F>
+__device__ __forceinline__ void load_x(uint32_t (&v)[4][4], const __half* x, bool two) {
 #pragma unroll
-    for (int i = 0; i < kW; ++i) {
-        if (F != few::kG128 && j + i >= 2 && !two) break;
-        const uint4 u = few::ld_global16(x + (few::x_chunk<F>(j + i, 0) - few::x_chunk<F>(0, 0)) * 8);
+    for (int i = 0; i < 4; ++i) {
+        if (F != few::kG128 && i >= 2 && !two) break;
+        const uint4 u = few::ld_global16(x + (few::x_chunk<F>(i, 0) - few::x_chunk<F>(0, 0)) * 8);
         v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
     }
 }
 
 // ------------------------------ gate and up ------------------------------
-template <int F, bool Z, int NT>
+template <int F, bool Z>
 __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs
     __shared__ Route R;
@@ -338,70 +331,60 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
         row[0] = static_cast<int64_t>(R.list[idx]) * 2 * p.f + (t0 + tile - idx * per_e) * 8 + g;
         row[1] = row[0] + p.f;
     };
-    few::Runner<F, Z, kDepth, NT, false> run;
+    few::Runner<F, Z, kDepth, 1, false> run;
     run.find(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
     run.start(w, rows_of);
 
-    Columns<NT> col;
-    const __half* x[NT];  // a lane's first chunk of its columns
+    Columns col;
+    const __half* x = nullptr;  // the lane's first chunk of its column
     auto begin = [&](int tile) {
-        if (!col.enter(R, (t0 + tile) / per_e, g)) return;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt] = p.xs + static_cast<int64_t>(R.pair_tok[col.pair[nt]]) * p.h + few::x_chunk<F>(0, t) * 8;
+        if (col.enter(R, (t0 + tile) / per_e, g)) x = p.xs + static_cast<int64_t>(R.pair_tok[col.pair]) * p.h + few::x_chunk<F>(0, t) * 8;
     };
     auto mul = [&](const uint8_t* entry, int step) {
-        Ahead<NT> q;
-        constexpr int kW = Ahead<NT>::kWords;
+        uint32_t q[4][4];
         const bool two = run.whole(w, step);
         const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
-        auto ahead = [&](int j) {
-            if (j % kW != 0) return;
+        load_x<F>(q, x + to, two);
+        few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, tab, bank, step, two, [&](int j, int, uint32_t(&v)[4]) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (NT == 1 || (col.live >> nt & 1)) load_x<F, kW>(q.v[nt], x[nt] + to, j, two);
-        };
-        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, bank, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = q.v[nt][j % kW][i];
+            for (int i = 0; i < 4; ++i) v[i] = q[j][i];
         });
     };
     auto finish = [&](int tile) {
         const int r = ((t0 + tile) % per_e) * 8 + g;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int j = nt * 8 + 2 * t + c;
-                float a = 0.0f;
-                int tok = 0;
-                if (j < col.cnt) {
-                    tok = R.pair_tok[col.base + j];
-                    const float down = p.xscale[tok];
-                    const float gate = run.acc[nt][c] * down, up = run.acc[nt][2 + c] * down;
-                    a = gate / (1.0f + expf(-gate)) * up * R.pair_prob[col.base + j];
-                    const int64_t o = static_cast<int64_t>(col.base + j) * p.f;
-                    const int place = p.act_paired ? (r & ~7) + paired(g) : r;
-                    p.act32[o + place] = a;
-                    p.act16[o + place] = __float2half_rn(a);
-                }
-                int big = __float_as_int(fabsf(a));
-                for (int s = 4; s < 32; s <<= 1) big = max(big, __shfl_xor_sync(kFull, big, s));
-                if (g == 0 && j < col.cnt) atomicMax(p.amax + tok, big);
+        for (int c = 0; c < 2; ++c) {
+            const int j = 2 * t + c;
+            float a = 0.0f;
+            int tok = 0;
+            if (j < col.cnt) {
+                tok = R.pair_tok[col.base + j];
+                const float down = p.xscale[tok];
+                const float gate = run.acc[0][c] * down, up = run.acc[0][2 + c] * down;
+                a = gate / (1.0f + expf(-gate)) * up * R.pair_prob[col.base + j];
+                const int64_t o = static_cast<int64_t>(col.base + j) * p.f;
+                const int place = p.act_paired ? (r & ~7) + paired(g) : r;
+                p.act32[o + place] = a;
+                p.act16[o + place] = __float2half_rn(a);
             }
+            int big = __float_as_int(fabsf(a));
+            for (int s = 4; s < 32; s <<= 1) big = max(big, __shfl_xor_sync(kFull, big, s));
+            if (g == 0 && j < col.cnt) atomicMax(p.amax + tok, big);
+        }
     };
     run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, mul, finish);
 }
 
 // --------------------------------- down ---------------------------------
 // As load_x, from fp32 and times a token's power of two.
-template <int F, int kW>
-__device__ __forceinline__ void load_wide(uint32_t (&v)[kW][4], const float* x, float up, int j, bool two) {
+template <int F>
+__device__ __forceinline__ void load_wide(uint32_t (&v)[4][4], const float* x, float up, bool two) {
 #pragma unroll
-    for (int i = 0; i < kW; ++i) {
-        if (F != few::kG128 && j + i >= 2 && !two) break;
+    for (int i = 0; i < 4; ++i) {
+        if (F != few::kG128 && i >= 2 && !two) break;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint4 u = few::ld_global16(x + (few::x_chunk<F>(j + i, 0) - few::x_chunk<F>(0, 0)) * 8 + 4 * k);
+            const uint4 u = few::ld_global16(x + (few::x_chunk<F>(i, 0) - few::x_chunk<F>(0, 0)) * 8 + 4 * k);
             const __half2 lo = __floats2half2_rn(__uint_as_float(u.x) * up, __uint_as_float(u.y) * up);
             const __half2 hi = __floats2half2_rn(__uint_as_float(u.z) * up, __uint_as_float(u.w) * up);
             v[i][2 * k] = *reinterpret_cast<const uint32_t*>(&lo);
@@ -413,7 +396,7 @@ __device__ __forceinline__ void load_wide(uint32_t (&v)[kW][4], const float* x, 
 // A CTA has a run of output rows; a tile is 16 of them with one chosen expert's f, its columns that
 // expert's pairs.  The products of a pair go to shared memory, and a token's are added there in the
 // order of its choices.
-template <int F, bool Z, int NT>
+template <int F, bool Z>
 __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs, the pairs' products
     __shared__ Route R;
@@ -441,7 +424,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
         // where the second half is another CTA's, the first takes its place and is not stored
         row[1] = row[0] + (grp + 1 < g1 ? 8 : 0);
     };
-    few::Runner<F, Z, kDepth, NT, false> run;
+    few::Runner<F, Z, kDepth, 1, false> run;
     run.find(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
     run.start(w, rows_of);
     grid_dependency_wait();
@@ -458,44 +441,32 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
     __syncthreads();
     const bool conv = wide != 0;
 
-    Columns<NT> col;
-    const __half* x[NT];  // a lane's first chunk of its columns
+    Columns col;
+    const __half* x = nullptr;  // the lane's first chunk of its column
     auto begin = [&](int tile) {
-        if (!col.enter(R, tile / row_tiles, g)) return;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt] = p.act16 + static_cast<int64_t>(col.pair[nt]) * p.f + few::x_chunk<F>(0, t) * 8;
+        if (col.enter(R, tile / row_tiles, g)) x = p.act16 + static_cast<int64_t>(col.pair) * p.f + few::x_chunk<F>(0, t) * 8;
     };
     auto mul = [&](const uint8_t* entry, int step) {
-        Ahead<NT> q;
-        constexpr int kW = Ahead<NT>::kWords;
+        uint32_t q[4][4];
         const bool two = run.whole(w, step);
         const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
-        auto ahead = [&](int j) {
-            if (j % kW != 0) return;
+        if (!conv) load_x<F>(q, x + to, two);
+        else load_wide<F>(q, p.act32 + (x - p.act16) + to, factor[R.pair_tok[col.pair]], two);
+        few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, tab, bank, step, two, [&](int j, int, uint32_t(&v)[4]) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (NT > 1 && !(col.live >> nt & 1)) continue;
-                if (!conv) load_x<F, kW>(q.v[nt], x[nt] + to, j, two);
-                else load_wide<F, kW>(q.v[nt], p.act32 + (x[nt] - p.act16) + to, factor[R.pair_tok[col.pair[nt]]], j, two);
-            }
-        };
-        few::multiply<F, Z, NT>(run.side, entry, run.places, run.acc, col.live, tab, bank, step, two, ahead, [&](int j, int nt, uint32_t(&v)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = q.v[nt][j % kW][i];
+            for (int i = 0; i < 4; ++i) v[i] = q[j][i];
         });
     };
     auto finish = [&](int tile) {
         const int r0 = (tile % row_tiles) * 16;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < 2; ++c) {
+            const int j = 2 * t + c;
+            if (j >= col.cnt) continue;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int j = nt * 8 + 2 * t + c;
-                if (j >= col.cnt) continue;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (r0 + 8 * i < (g1 - g0) * 8) part[(col.base + j) * p.part_rows + r0 + 8 * i + g] = run.acc[nt][2 * i + c];
-            }
+            for (int i = 0; i < 2; ++i)
+                if (r0 + 8 * i < (g1 - g0) * 8) part[(col.base + j) * p.part_rows + r0 + 8 * i + g] = run.acc[0][2 * i + c];
+        }
     };
     run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, mul, finish);
     __syncthreads();
@@ -580,13 +551,13 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
     p.act16 = reinterpret_cast<__half*>(base + l.act16);
     p.x_paired = gate_up.integer ? 1 : 0;
     p.act_paired = down.integer ? 1 : 0;
-#define NF4_MOE_FORMS(K, ...)                                                                                                  \
-    {reinterpret_cast<const void*>(&K<few::kTable, false, __VA_ARGS__>), reinterpret_cast<const void*>(&K<few::kG128, false, __VA_ARGS__>), \
-     reinterpret_cast<const void*>(&K<few::kG128, true, __VA_ARGS__>),   reinterpret_cast<const void*>(&K<few::kG64, false, __VA_ARGS__>),  \
-     reinterpret_cast<const void*>(&K<few::kG64, true, __VA_ARGS__>),    reinterpret_cast<const void*>(&K<few::kG32, false, __VA_ARGS__>),  \
-     reinterpret_cast<const void*>(&K<few::kG32, true, __VA_ARGS__>)}
-    static const void* const up_fns[2][7] = {NF4_MOE_FORMS(k_moe_gate_up, 1), NF4_MOE_FORMS(k_moe_gate_up, 2)};
-    static const void* const down_fns[2][7] = {NF4_MOE_FORMS(k_moe_down, 1), NF4_MOE_FORMS(k_moe_down, 2)};
+#define NF4_MOE_FORMS(K)                                                                                        \
+    {reinterpret_cast<const void*>(&K<few::kTable, false>), reinterpret_cast<const void*>(&K<few::kG128, false>), \
+     reinterpret_cast<const void*>(&K<few::kG128, true>),   reinterpret_cast<const void*>(&K<few::kG64, false>),  \
+     reinterpret_cast<const void*>(&K<few::kG64, true>),    reinterpret_cast<const void*>(&K<few::kG32, false>),  \
+     reinterpret_cast<const void*>(&K<few::kG32, true>)}
+    static const void* const up_fns[7] = NF4_MOE_FORMS(k_moe_gate_up);
+    static const void* const down_fns[7] = NF4_MOE_FORMS(k_moe_down);
 #undef NF4_MOE_FORMS
     for (int64_t t = 0; t < m; t += kMaxM) {
         p.m = static_cast<int>(m - t < kMaxM ? m - t : kMaxM);
@@ -600,15 +571,14 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
         if (e != cudaSuccess) return e;
 
         int fit = 0;
-        const int nt = p.m > 8 ? 2 : 1;
-        const int64_t chosen = E < p.m * top ? E : p.m * top;  // at most
+        const int64_t chosen = E < p.m * top ? E : p.m * top;  // at most, but for experts of more than eight tokens
         auto warps_of = [&](int64_t steps) { return steps <= few::kFewSteps ? few::kFewWarps : few::kMaxWarps; };
         auto arrange = [&](const MoeWeight& w, int warps) {
             p.ring_at = w.integer ? 0 : few::kTableBytes;
             p.slots_at = p.ring_at + warps * kDepth * few::kStepBytes;
-            p.part_at = p.slots_at + warps * nt * 512;
+            p.part_at = p.slots_at + warps * 512;
         };
-        const void* fn = up_fns[nt - 1][form_of(gate_up)];
+        const void* fn = up_fns[form_of(gate_up)];
         if ((e = few::resident(fn, 1, dev, &fit)) != cudaSuccess) return e;
         int64_t grid = chosen * (f / 8) < fit ? chosen * (f / 8) : fit;
         int warps = warps_of((chosen * (f / 8) + grid - 1) / grid * ((h + few::kStepK - 1) / few::kStepK));
@@ -616,7 +586,7 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
         if ((e = few::launch(fn, grid, warps * 32, p.part_at, 1, stream, args)) != cudaSuccess) return e;
 
         // down: so many output rows a CTA that the pairs' products fit
-        fn = down_fns[nt - 1][form_of(down)];
+        fn = down_fns[form_of(down)];
         if ((e = few::resident(fn, 1, dev, &fit)) != cudaSuccess) return e;
         grid = h / 8 < fit ? h / 8 : fit;
         warps = warps_of(((h / 8 + grid - 1) / grid + 1) / 2 * chosen * ((f + few::kStepK - 1) / few::kStepK));
