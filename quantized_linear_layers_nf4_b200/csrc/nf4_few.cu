@@ -6,7 +6,7 @@
 namespace nf4 {
 namespace few {
 
-cudaError_t resident(const void* fn, int splits, const DeviceInfo& dev, int* out) {
+cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& dev, int* out) {
     struct Known {
         const void* fn;
         int device, splits, clusters;
@@ -26,7 +26,7 @@ cudaError_t resident(const void* fn, int splits, const DeviceInfo& dev, int* out
     if (splits > 1) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / splits * splits));
-        cfg.blockDim = dim3(kMaxThreads);
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
         cfg.dynamicSmemBytes = kMaxSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -39,14 +39,12 @@ namespace nf4 {
 namespace few {
 
 constexpr int kItemK = 64;   // the unit that k is a multiple of
-constexpr int kStepK = 128;  // k of a step; its second half may lie past the end of k
+constexpr int kStepK = 128;  // k of a step; its second half may lie past the end of k (see multiply)
 constexpr int kStepBytes = 16 * kStepK / 2;
 
-// Warps of a CTA.  24 fill an SM (80 registers a thread); a call that gives a CTA few steps
-// takes 12, so that the next kernel's CTAs find room and start while its last ones run.
-constexpr int kMaxWarps = 24, kFewWarps = 12;
-constexpr int kFewSteps = 96;  // of a CTA: up to here kFewWarps
-constexpr int kMaxThreads = kMaxWarps * 32;
+// A kernel's CTA has either W warps, which fill an SM, or half of them where a call gives it
+// few steps, so that the next kernel's CTAs find room and start while its last ones run.
+constexpr int kFewSteps = 96;  // of a CTA: up to here half the warps
 
 // The warp's number as a value that the compiler sees to be one for all its lanes.
 __device__ __forceinline__ int warp_index() { return static_cast<int>(__reduce_max_sync(kFull, threadIdx.x >> 5)); }
@@ -172,6 +170,7 @@ struct Sides {
     const float* e[2];    // kTable: scale of the rows' first absmax code, and that code's place under it
     uint32_t at[2];
     uint32_t raw_s[2], raw_z[2];  // of the next window, as loaded: anything done to it would wait for it
+    bool past;            // the lane's group of it is past the end of k
     float f[2];           // of this window
     uint32_t zz[2];       // zero points of this window, in both halves
 
@@ -190,6 +189,7 @@ struct Sides {
         }
     }
     __device__ __forceinline__ void load(const Weight& w, int window, int t) {
+        past = F != kG128 && 4 * window + t >= w.units;
         const uint32_t unit = min(4 * window + t, w.units - 1);
         if (F == kTable) {
 #pragma unroll
@@ -219,6 +219,7 @@ struct Sides {
         for (int i = 0; i < 2; ++i) {
             if (F == kTable) f[i] = absmax_hat(static_cast<int>(raw_z[i]), __uint_as_float(raw_s[i]), mu);
             else f[i] = __uint_as_float(raw_s[i] << (w.f32 ? 0 : 16));
+            if (F != kG128 && past) f[i] = 0.0f;
             if (Z) zz[i] = prmt(raw_z[i], 0u, 0x4040) & 0x000f000fu;
         }
     }
@@ -278,7 +279,8 @@ __device__ __forceinline__ void ring_words(const uint8_t* entry, const Places& a
 }
 
 // A word as four fp16 pairs; zz: the zero point in both halves; tab: the table, bank: the lane's
-// copy of it (4 lane).
+// copy of it (4 lane).  Every fourth word decoded by byte permutes instead, to spare the shared
+// memory, took a tenth longer.
 template <int F>
 __device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* tab, uint32_t bank, uint32_t (&o)[4]) {
     if (F == kTable) {
@@ -293,48 +295,65 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t zz, const uint8_t* t
 }
 
 // acc += (16 rows x 128 k of W) x (128 k x 8 NT columns of X); x(j, nt, v) gives the lane's
-// eight values of word j, column g of n-tile nt.  `step`: counted from the row's first.
+// eight values of word j, column g of n-tile nt.  `step`: counted from the row's first.  Where k ends
+// in the middle of a step, the second half's codes are any, their scales 0 and their X 0.
 template <int F, bool Z, int NT, typename XF>
 __device__ __forceinline__ void multiply(const Sides<F, Z>& side, const uint8_t* entry, const Places& at, float (&acc)[NT][4],
-                                         const uint8_t* tab, uint32_t bank, int step, bool two, XF&& x) {
+                                         const uint8_t* tab, uint32_t bank, int step, XF&& x) {
     uint32_t c[2][4];
     ring_words<F>(entry, at, c[0]);
     ring_words<F>(entry + 512, at, c[1]);
     constexpr int kR = window_steps<F>(), kU = 4 / kR;
     const int unit = static_cast<int>(static_cast<unsigned>(step) % kR * kU);  // of the step's first group
-    float p[NT][4], f[2] = {0.0f, 0.0f};
-    uint32_t zz[2] = {0x00080008u, 0x00080008u};
+    // words j and j + 2 side by side: their sums do not wait for each other's products
+    float p[2][NT][4], f[2][2];
+    uint32_t zz[2][2] = {{0x00080008u, 0x00080008u}, {0x00080008u, 0x00080008u}};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (F != kG128 && j == 2 && !two) return;
-        const bool first = F == kG128 ? j == 0 : (F == kG32 || (j & 1) == 0);
-        const bool last = F == kG128 ? j == 3 : (F == kG32 || (j & 1) == 1);
-        if (first) {
+    for (int j = 0; j < 2; ++j) {
+        constexpr bool kEach = F == kG32;  // a group ends with every word
+        uint32_t a[2][4], b[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f[i] = __shfl_sync(kFull, side.f[i], unit + j * kU / 4, 4);
-                if (Z) zz[i] = __shfl_sync(kFull, side.zz[i], unit + j * kU / 4, 4);
+        for (int h = 0; h < 2; ++h) {
+            if (kEach || j == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int from = unit + (j + 2 * h) * kU / 4;
+                    if (F == kG128 && h == 1) {
+                        f[h][i] = f[0][i];
+                        zz[h][i] = zz[0][i];
+                    } else {
+                        f[h][i] = __shfl_sync(kFull, side.f[i], from, 4);
+                        if (Z) zz[h][i] = __shfl_sync(kFull, side.zz[i], from, 4);
+                    }
+                }
             }
+            decode<F>(c[0][j + 2 * h], zz[h][0], tab, bank, a[h]);
+            decode<F>(c[1][j + 2 * h], zz[h][1], tab, bank, b[h]);
         }
-        uint32_t a[4], b[4];
-        decode<F>(c[0][j], zz[0], tab, bank, a);
-        decode<F>(c[1][j], zz[1], tab, bank, b);
+        uint32_t v[2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            uint32_t v[4];
-            x(j, nt, v);
-            if (first) mma_f16_first(p[nt], a[0], b[0], a[1], b[1], v[0], v[1]);
-            else mma_f16(p[nt], a[0], b[0], a[1], b[1], v[0], v[1]);
-            mma_f16(p[nt], a[2], b[2], a[3], b[3], v[2], v[3]);
-        }
-        if (last) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                    acc[nt][0] = __fmaf_rn(f[0], p[nt][0], acc[nt][0]);
-                acc[nt][1] = __fmaf_rn(f[0], p[nt][1], acc[nt][1]);
-                acc[nt][2] = __fmaf_rn(f[1], p[nt][2], acc[nt][2]);
-                acc[nt][3] = __fmaf_rn(f[1], p[nt][3], acc[nt][3]);
-            }
+            for (int nt = 0; nt < NT; ++nt) x(j + 2 * h, nt, v[h][nt]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)  // the two products of a word
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (i == 0 && (kEach || j == 0)) mma_f16_first(p[h][nt], a[h][0], b[h][0], a[h][1], b[h][1], v[h][nt][0], v[h][nt][1]);
+                    else mma_f16(p[h][nt], a[h][2 * i], b[h][2 * i], a[h][2 * i + 1], b[h][2 * i + 1], v[h][nt][2 * i], v[h][nt][2 * i + 1]);
+                }
+        if (kEach || j == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    acc[nt][0] = __fmaf_rn(f[h][0], p[h][nt][0], acc[nt][0]);
+                    acc[nt][1] = __fmaf_rn(f[h][0], p[h][nt][1], acc[nt][1]);
+                    acc[nt][2] = __fmaf_rn(f[h][1], p[h][nt][2], acc[nt][2]);
+                    acc[nt][3] = __fmaf_rn(f[h][1], p[h][nt][3], acc[nt][3]);
+                }
         }
     }
 }
@@ -372,9 +391,9 @@ __device__ __forceinline__ uint32_t x_flip(int t) {
 // X [m] rows of `per` chunks, `row` chunks apart, into shared memory as fp16, each token times the power
 // of two that its largest value here asks for (top[token]: that value's bf16 magnitude), in the order of
 // int4_f16's pairs.  All threads; m is at most the number of warps, which are dealt out evenly to
-// the tokens (1 << lg of them each).  Ends with a block barrier.
+// the tokens (1 << lg of them each).  Up to `padded` chunks it is zeros.  Ends with a block barrier.
 template <int F>
-__device__ __forceinline__ void stage_x(const uint4* x, int row, int per, int m, int lg, uint8_t* out, int stride, uint32_t* top, int warp,
+__device__ __forceinline__ void stage_x(const uint4* x, int row, int per, int padded, int m, int lg, uint8_t* out, int stride, uint32_t* top, int warp,
                                         int lane, int warps) {
     constexpr int kBatch = 8;  // loads in flight
     if (threadIdx.x < warps) top[threadIdx.x] = 0;
@@ -407,6 +426,7 @@ __device__ __forceinline__ void stage_x(const uint4* x, int row, int per, int m,
     if (tok < m) {
         const float up = scale_up(scale_exponent(static_cast<int>(top[tok] >> 7)));
         const bool again = end > kBatch * hop;  // more than one batch: from L1 this time
+        for (int c = per + first; c < padded; c += hop) *reinterpret_cast<uint4*>(out + tok * stride + x_place<F>(c)) = make_uint4(0u, 0u, 0u, 0u);
         for (int c = first; c - lane < end; c += kBatch * hop) {
             if (again) load(c);
 #pragma unroll
@@ -431,9 +451,10 @@ __host__ __device__ inline Shares shares_of(int total, int parts) {
     const int each = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(parts));
     return Shares{each, total - each * parts};
 }
-// Over the warps of a CTA, of which there are two numbers: no division by a variable.
+// Over the warps of a CTA, W or half as many: no division by a variable.
+template <int W>
 __device__ __forceinline__ Shares shares_of_warps(int total) {
-    return blockDim.x == kFewWarps * 32 ? shares_of(total, kFewWarps) : shares_of(total, kMaxWarps);
+    return blockDim.x == W * 16 ? shares_of(total, W / 2) : shares_of(total, W);
 }
 
 // ------------------------------ runs of steps ------------------------------
@@ -442,6 +463,7 @@ __device__ __forceinline__ Shares shares_of_warps(int total) {
 // share, the warp that begins it adds the others' sums, in warp order, from `slots`.
 //   rows(tile, row)      the lane's two rows of a tile
 //   begin(tile)          as a tile is entered
+//   ahead(step)          before the step's codes are waited for
 //   mul(entry, step)     multiplies a step of the tile, counted from the row's first
 //   finish(tile)         its sums are complete in acc
 // kFour: the inner loop takes four steps at a time where it can; without it the code and its
@@ -465,14 +487,13 @@ struct Runner {
 #pragma unroll
         for (int i = 0; i < 2; ++i) c[i] = w.wq + row[i] * (w.k >> 1) + 16 * t;
     }
-    __device__ __forceinline__ bool whole(const Weight& w, int st) const {  // a step's second half is not past the end of k
-        return F == kG128 || (st + 1) * kStepK <= w.k;
-    }
-    __device__ __forceinline__ void copy(uint32_t entry, uint64_t to, bool two) const {
+    __device__ __forceinline__ void copy(const Weight& w, uint32_t entry, uint32_t to) const {
+        const bool in = F == kG128 || to + 16u * t < static_cast<uint32_t>(w.k >> 1);  // else past the end of k: zeros
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (F == kG128) copy16(put + entry + 512 * i, c[i] + to);
-            else copy16(put + entry + 512 * i, c[i] + to, two || t < 2 ? 16 : 0);
+            const uint8_t* p = c[i] + static_cast<uint64_t>(to);
+            if (F == kG128) copy16(put + entry + 512 * i, p);
+            else copy16(put + entry + 512 * i, p, in ? 16 : 0);
         }
     }
     template <typename Rows>
@@ -492,7 +513,7 @@ struct Runner {
     template <typename Rows>
     __device__ __forceinline__ void send(const Weight& w, uint32_t entry, Rows&& rows) {
         if (sent < i1) {
-            copy(entry, static_cast<uint32_t>(step) * (kStepK / 2u), whole(w, step));
+            copy(w, entry, static_cast<uint32_t>(step) * (kStepK / 2u));
             moved(w, 1, rows);
         }
         copies_commit();
@@ -548,9 +569,9 @@ struct Runner {
         for (int nt = 0; nt < NT; ++nt) slots[(warp * NT + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
     }
     // All threads of the block; ns > 0.
-    template <typename Rows, typename Begin, typename Mul, typename Finish>
-    __device__ __forceinline__ void run(const Weight& w, float mu, float4* slots, const Shares& runs, Rows&& rows, Begin&& begin, Mul&& mul,
-                                        Finish&& finish) {
+    template <typename Rows, typename Begin, typename Ahead, typename Mul, typename Finish>
+    __device__ __forceinline__ void run(const Weight& w, float mu, float4* slots, const Shares& runs, Rows&& rows, Begin&& begin,
+                                        Ahead&& ahead, Mul&& mul, Finish&& finish) {
         int tl = static_cast<int>(static_cast<unsigned>(i0) / static_cast<unsigned>(ns)), st = i0 - tl * ns;
         uint32_t entry = 0;
         bool mine = st == 0;  // this warp begins the tile
@@ -564,7 +585,8 @@ struct Runner {
                 next_window(w, rows);
             };
             auto wrap = [&] { entry = entry == (kDepth - 1) * kStepBytes ? 0u : entry + kStepBytes; };
-            auto ready = [&] {
+            auto ready = [&](int step) {
+                ahead(step);
                 copies_wait<kDepth - 1>();
                 if (F != kG128) __syncwarp();  // else a lane reads what it copied itself
             };
@@ -574,16 +596,16 @@ struct Runner {
                     // four steps from a multiple of four on: windows and offsets are constants, and
                     // as a rule the four that follow are one more piece of the same rows
                     const unsigned q = static_cast<unsigned>(st) >> 2;
-                    const bool plain = sent + 4 <= i1 && step + 4 <= s0 + ns && whole(w, step + 3);
+                    const bool plain = sent + 4 <= i1 && step + 4 <= s0 + ns;
                     const uint32_t to = static_cast<uint32_t>(step) * (kStepK / 2u);
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         if (s > 0 && s % kR == 0) turn();
-                        ready();
+                        ready(static_cast<int>(4 * q + s));
                         mul(ring + entry, static_cast<int>(4 * q + s));
                         if (F != kG128) __syncwarp();
                         if (plain) {
-                            copy(entry, to + s * (kStepK / 2u), true);
+                            copy(w, entry, to + s * (kStepK / 2u));
                             copies_commit();
                         } else {
                             send(w, entry, rows);
@@ -593,7 +615,7 @@ struct Runner {
                     if (plain) moved(w, 4, rows);
                     st += 4;
                 } else {
-                    ready();
+                    ready(st);
                     mul(ring + entry, st);
                     if (F != kG128) __syncwarp();
                     send(w, entry, rows);

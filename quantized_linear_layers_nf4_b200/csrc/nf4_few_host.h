@@ -12,7 +12,7 @@ constexpr int kMaxSmem = 216 * 1024;  // dynamic shared memory these kernels may
 // Clusters of `splits` (1, 2, 4, 8) CTAs, one CTA an SM, that the current device runs at
 // the same time; also allows the kernel its dynamic shared memory.  Asked of the runtime
 // once per kernel, device and size.
-cudaError_t resident(const void* fn, int splits, const DeviceInfo& dev, int* out);
+cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& dev, int* out);
 
 inline Weight int4_weight(const Int4Args& w) {
     Weight o = {};

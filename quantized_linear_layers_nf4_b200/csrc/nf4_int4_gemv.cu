@@ -19,6 +19,8 @@
 namespace nf4 {
 namespace int4 {
 
+constexpr int kWarps = 16;  // 128 registers a thread; 24 warps of 80 took a tenth longer
+
 // Steps on their way in a warp: sixteen tokens' X and sums leave room for three.
 constexpr int depth_of(int nt) { return nt == 1 ? 4 : 3; }
 
@@ -37,9 +39,9 @@ struct GemvArgs {
 };
 
 template <int F, bool Z, int NT>
-__global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_constant__ GemvArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 1) k_int4_gemv(const __grid_constant__ GemvArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];  // X, the ring, sums of runs, the CTA's sums
-    __shared__ uint32_t top[few::kMaxWarps];  // bf16 magnitude of a token's largest value in this CTA's range of k
+    __shared__ uint32_t top[kWarps];  // bf16 magnitude of a token's largest value in this CTA's range of k
     float* part = reinterpret_cast<float*>(smem + a.part_at);
 
     const int warp = few::warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -48,7 +50,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
     const int g0 = a.rows.start(cl), g1 = a.rows.start(cl + 1);
     const int s0 = a.ks.start(rank), ns = a.ks.start(rank + 1) - s0;  // steps of a tile
     const int warps = blockDim.x >> 5;
-    const few::Shares runs = few::shares_of_warps((g1 - g0 + 1) / 2 * ns);
+    const few::Shares runs = few::shares_of_warps<kWarps>((g1 - g0 + 1) / 2 * ns);
     auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int grp = g0 + tile * 2;
         // where a run's last tile has one group, that takes the place of another CTA's, and rows
@@ -64,8 +66,8 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
     grid_launch_dependents();
     // this CTA's k range of X
     const int first = s0 * (few::kStepK / 8);
-    few::stage_x<F>(reinterpret_cast<const uint4*>(a.x) + first, a.w.k / 8, min((s0 + ns) * (few::kStepK / 8), a.w.k / 8) - first, a.m,
-                    a.x_lg, smem, a.x_stride, top, warp, lane, warps);
+    few::stage_x<F>(reinterpret_cast<const uint4*>(a.x) + first, a.w.k / 8, min((s0 + ns) * (few::kStepK / 8), a.w.k / 8) - first,
+                    ns * (few::kStepK / 8), a.m,                    a.x_lg, smem, a.x_stride, top, warp, lane, warps);
 
     const uint8_t* xb[NT][2];  // columns past m read the last token's: their sums are not stored
 #pragma unroll
@@ -75,7 +77,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
     }
     auto mul = [&](const uint8_t* entry, int step) {
         const uint32_t x0 = (step - s0) * (few::kStepK * 2);
-        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, nullptr, 0u, step, R.whole(a.w, step), [&](int j, int nt, uint32_t(&v)[4]) {
+        few::multiply<F, Z, NT>(R.side, entry, R.places, R.acc, nullptr, 0u, step, [&](int j, int nt, uint32_t(&v)[4]) {
             const uint4 u = *reinterpret_cast<const uint4*>(xb[nt][j >> 1] + x0 + few::x_word<F>(j));
             v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
         });
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_int4_gemv(const __grid_
                 }
             }
     };
-    R.run(a.w, 0.0f, reinterpret_cast<float4*>(smem + a.slots_at), runs, rows_of, [](int) {}, mul, finish);
+    R.run(a.w, 0.0f, reinterpret_cast<float4*>(smem + a.slots_at), runs, rows_of, [](int) {}, [](int) {}, mul, finish);
     if (a.splits == 1) return;
     cluster_sync();
     const uint32_t base = smem_u32(part);
@@ -153,13 +155,14 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     // k is split over a cluster where a CTA's share of X would take long to bring in (64 KB),
     // or where there are fewer row groups than SMs and each part still feeds the warps
     int splits = 1;
-    while (splits < 8 && (m * w.k * 2 / splits > 64 * 1024 || (groups * splits * 2 <= dev.sm_count && all >= splits * 2 * few::kFewWarps))) splits *= 2;
+    while (splits < 8 && (m * w.k * 2 / splits > 64 * 1024 || (groups * splits * 2 <= dev.sm_count && all >= splits * kWarps))) splits *= 2;
     int fit = 0;
-    cudaError_t e = few::resident(fn, splits, dev, &fit);
+    cudaError_t e = few::resident(fn, kWarps * 32, splits, dev, &fit);
     if (e != cudaSuccess) return e;
     int64_t clusters = fit < groups ? fit : groups;
     const int64_t steps = ((groups + clusters - 1) / clusters + 1) / 2 * ((all + splits - 1) / splits);
-    const int warps = steps <= (m > 4 ? 1 : 2) * few::kFewSteps && m <= few::kFewWarps ? few::kFewWarps : few::kMaxWarps;  // a warp or more a token for X
+    // m = 4 is about where what a warp costs at its start outweighs what it adds
+    const int warps = steps <= (m > 4 ? 1 : 2) * few::kFewSteps && m <= kWarps / 2 ? kWarps / 2 : kWarps;  // a warp or more a token for X
     const Room at = room_of(m, w.k, splits, fmt, warps);
     if (at.left < m * 64) return cudaErrorInvalidConfiguration;
     while (splits > 1 && (groups + clusters - 1) / clusters * 8 * m * 4 > at.left) clusters += fit;
@@ -189,7 +192,7 @@ cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* 
     // so many tokens at a time that an eighth of their X leaves room for 16 KB of sums (all
     // sixteen up to k = 26624, eight to 47104, then four)
     int64_t most = kGemvMaxTokens;
-    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w), few::kMaxWarps).left < 16 * 1024) most /= 2;
+    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w), int4::kWarps).left < 16 * 1024) most /= 2;
     for (int64_t t = 0; t < m; t += most) {
         const cudaError_t e = launch_int4_gemv_pass(static_cast<const char*>(X) + t * w.k * 2, m - t < most ? m - t : most, w,
                                                     static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, dev, stream);

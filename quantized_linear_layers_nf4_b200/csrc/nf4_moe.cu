@@ -33,20 +33,21 @@ constexpr int kMaxM = 16;  // tokens of a pass
 constexpr int kMaxTop = 16;
 constexpr int kMaxE = 512;
 constexpr int kMaxPairs = kMaxM * kMaxTop;
+constexpr int kWarps = 20;  // 96 registers a thread; 16 and 24 warps took a few percent longer
 constexpr int kDepth = 3;  // steps on their way in a warp, beside the table of levels
 
 struct Params {
     const __nv_bfloat16* x;
     const __nv_bfloat16* router;
     int m, E, top;
-    int h, f;
+    int h, f, hp, fp;
     int renormalize;
     few::Weight gate_up, down;
     float* logits;   // [m][E]
-    __half* xs;      // [m][h]
+    __half* xs;      // [m][hp], hp = h and fp = f up to whole steps: zeros behind the end
     float* xscale;   // [m]
     int* amax;       // [m] bits of the largest |a| of a token
-    float* act32;    // [m * top][f], the pairs of an expert together
+    float* act32;    // [m * top][fp], the pairs of an expert together
     __half* act16;
     __nv_bfloat16* y;
     int32_t* ids;    // [m][top] or null
@@ -123,7 +124,14 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const __grid_cons
         p.xscale[t] = few::scale_down(ex);
         p.amax[t] = 0;
     }
-    __half* xs = p.xs + static_cast<int64_t>(t) * p.h;
+    __half* xs = p.xs + static_cast<int64_t>(t) * p.hp;
+    for (int c = chunks + tid; c < p.hp / 8; c += kRouterThreads) reinterpret_cast<uint4*>(xs)[c] = make_uint4(0u, 0u, 0u, 0u);
+    // behind the end of f, of the activations to come
+    for (int i = tid; i < p.top * (p.fp - p.f); i += kRouterThreads) {
+        const int64_t o = (static_cast<int64_t>(t) * p.top + i / (p.fp - p.f)) * p.fp + p.f + i % (p.fp - p.f);
+        p.act32[o] = 0.0f;
+        p.act16[o] = __float2half_rn(0.0f);
+    }
     for (int c = tid; c < chunks; c += kRouterThreads) {
         const uint4 v = few::ld_global16(x + c);
         uint32_t u[4] = {v.x, v.y, v.z, v.w}, o[4];
@@ -290,10 +298,9 @@ struct Columns {
 // A lane's X of a step, from global memory through L1, `x` its first chunk: all of it is asked
 // for before the first word is decoded.
 template <int F>
-__device__ __forceinline__ void load_x(uint32_t (&v)[4][4], const __half* x, bool two) {
+__device__ __forceinline__ void load_x(uint32_t (&v)[4][4], const __half* x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (F != few::kG128 && i >= 2 && !two) break;
         const uint4 u = few::ld_global16(x + (few::x_chunk<F>(i, 0) - few::x_chunk<F>(0, 0)) * 8);
         v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
     }
@@ -301,7 +308,7 @@ __device__ __forceinline__ void load_x(uint32_t (&v)[4][4], const __half* x, boo
 
 // ------------------------------ gate and up ------------------------------
 template <int F, bool Z>
-__global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) k_moe_gate_up(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs
     __shared__ Route R;
 
@@ -318,13 +325,12 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
 
     const few::Weight& w = p.gate_up;
     const float mu = F == few::kTable ? __ldg(w.mu) : 0.0f;
-    const uint8_t* tab = smem;
     const uint32_t bank = 4 * lane;
     const int per_e = p.f / 8;
     const few::Shares mine = few::shares_of(R.active * per_e, gridDim.x);
     const int t0 = mine.start(blockIdx.x), t1 = mine.start(blockIdx.x + 1);
     const int ns = (p.h + few::kStepK - 1) / few::kStepK;
-    const few::Shares runs = few::shares_of_warps((t1 - t0) * ns);
+    const few::Shares runs = few::shares_of_warps<kWarps>((t1 - t0) * ns);
 
     auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int idx = (t0 + tile) / per_e;
@@ -338,14 +344,15 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
     Columns col;
     const __half* x = nullptr;  // the lane's first chunk of its column
     auto begin = [&](int tile) {
-        if (col.enter(R, (t0 + tile) / per_e, g)) x = p.xs + static_cast<int64_t>(R.pair_tok[col.pair]) * p.h + few::x_chunk<F>(0, t) * 8;
+        if (col.enter(R, (t0 + tile) / per_e, g)) x = p.xs + static_cast<int64_t>(R.pair_tok[col.pair]) * p.hp + few::x_chunk<F>(0, t) * 8;
+    };
+    uint32_t q[4][4];
+    auto ahead = [&](int step) {
+        const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
+        load_x<F>(q, x + to);
     };
     auto mul = [&](const uint8_t* entry, int step) {
-        uint32_t q[4][4];
-        const bool two = run.whole(w, step);
-        const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
-        load_x<F>(q, x + to, two);
-        few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, tab, bank, step, two, [&](int j, int, uint32_t(&v)[4]) {
+        few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, smem, bank, step, [&](int j, int, uint32_t(&v)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = q[j][i];
         });
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
                 const float down = p.xscale[tok];
                 const float gate = run.acc[0][c] * down, up = run.acc[0][2 + c] * down;
                 a = gate / (1.0f + expf(-gate)) * up * R.pair_prob[col.base + j];
-                const int64_t o = static_cast<int64_t>(col.base + j) * p.f;
+                const int64_t o = static_cast<int64_t>(col.base + j) * p.fp;
                 const int place = p.act_paired ? (r & ~7) + paired(g) : r;
                 p.act32[o + place] = a;
                 p.act16[o + place] = __float2half_rn(a);
@@ -372,16 +379,15 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_gate_up(const __gri
             if (g == 0 && j < col.cnt) atomicMax(p.amax + tok, big);
         }
     };
-    run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, mul, finish);
+    run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, ahead, mul, finish);
 }
 
 // --------------------------------- down ---------------------------------
 // As load_x, from fp32 and times a token's power of two.
 template <int F>
-__device__ __forceinline__ void load_wide(uint32_t (&v)[4][4], const float* x, float up, bool two) {
+__device__ __forceinline__ void load_wide(uint32_t (&v)[4][4], const float* x, float up) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (F != few::kG128 && i >= 2 && !two) break;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint4 u = few::ld_global16(x + (few::x_chunk<F>(i, 0) - few::x_chunk<F>(0, 0)) * 8 + 4 * k);
@@ -397,7 +403,7 @@ __device__ __forceinline__ void load_wide(uint32_t (&v)[4][4], const float* x, f
 // expert's pairs.  The products of a pair go to shared memory, and a token's are added there in the
 // order of its choices.
 template <int F, bool Z>
-__global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) k_moe_down(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];  // levels, the ring, sums of runs, the pairs' products
     __shared__ Route R;
     __shared__ float factor[kMaxM];
@@ -411,12 +417,11 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
 
     const few::Weight& w = p.down;
     const float mu = F == few::kTable ? __ldg(w.mu) : 0.0f;
-    const uint8_t* tab = smem;
     const uint32_t bank = 4 * lane;
     const int g0 = p.rows.start(blockIdx.x), g1 = p.rows.start(blockIdx.x + 1);
     const int row_tiles = (g1 - g0 + 1) / 2;
     const int ns = (p.f + few::kStepK - 1) / few::kStepK;
-    const few::Shares runs = few::shares_of_warps(R.active * row_tiles * ns);
+    const few::Shares runs = few::shares_of_warps<kWarps>(R.active * row_tiles * ns);
 
     auto rows_of = [&](int tile, int64_t(&row)[2]) {
         const int idx = tile / row_tiles, grp = g0 + (tile - idx * row_tiles) * 2;
@@ -444,15 +449,16 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
     Columns col;
     const __half* x = nullptr;  // the lane's first chunk of its column
     auto begin = [&](int tile) {
-        if (col.enter(R, tile / row_tiles, g)) x = p.act16 + static_cast<int64_t>(col.pair) * p.f + few::x_chunk<F>(0, t) * 8;
+        if (col.enter(R, tile / row_tiles, g)) x = p.act16 + static_cast<int64_t>(col.pair) * p.fp + few::x_chunk<F>(0, t) * 8;
+    };
+    uint32_t q[4][4];
+    auto ahead = [&](int step) {
+        const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
+        if (!conv) load_x<F>(q, x + to);
+        else load_wide<F>(q, p.act32 + (x - p.act16) + to, factor[R.pair_tok[col.pair]]);
     };
     auto mul = [&](const uint8_t* entry, int step) {
-        uint32_t q[4][4];
-        const bool two = run.whole(w, step);
-        const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
-        if (!conv) load_x<F>(q, x + to, two);
-        else load_wide<F>(q, p.act32 + (x - p.act16) + to, factor[R.pair_tok[col.pair]], two);
-        few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, tab, bank, step, two, [&](int j, int, uint32_t(&v)[4]) {
+        few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, smem, bank, step, [&](int j, int, uint32_t(&v)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = q[j][i];
         });
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(few::kMaxThreads, 1) k_moe_down(const __grid_c
                 if (r0 + 8 * i < (g1 - g0) * 8) part[(col.base + j) * p.part_rows + r0 + 8 * i + g] = run.acc[0][2 * i + c];
         }
     };
-    run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, mul, finish);
+    run.run(w, mu, reinterpret_cast<float4*>(smem + p.slots_at), runs, rows_of, begin, ahead, mul, finish);
     __syncthreads();
     const int rows = (g1 - g0) * 8;
     for (int i = threadIdx.x; i < p.m * rows; i += blockDim.x) {
@@ -486,7 +492,10 @@ static size_t round256(size_t v) { return (v + 255) & ~static_cast<size_t>(255);
 struct Layout {
     size_t logits, xs, xscale, amax, act32, act16, total;
 };
+static int64_t whole_steps(int64_t k) { return (k + few::kStepK - 1) / few::kStepK * few::kStepK; }
 static Layout layout(int64_t h, int64_t f, int E, int top) {
+    h = whole_steps(h);
+    f = whole_steps(f);
     Layout l;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -540,6 +549,8 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
     p.top = top;
     p.h = static_cast<int>(h);
     p.f = static_cast<int>(f);
+    p.hp = static_cast<int>(whole_steps(h));
+    p.fp = static_cast<int>(whole_steps(f));
     p.renormalize = renormalize ? 1 : 0;
     p.gate_up = weight_of(gate_up);
     p.down = weight_of(down);
@@ -572,14 +583,14 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
 
         int fit = 0;
         const int64_t chosen = E < p.m * top ? E : p.m * top;  // at most, but for experts of more than eight tokens
-        auto warps_of = [&](int64_t steps) { return steps <= few::kFewSteps ? few::kFewWarps : few::kMaxWarps; };
+        auto warps_of = [&](int64_t steps) { return steps <= few::kFewSteps ? kWarps / 2 : kWarps; };
         auto arrange = [&](const MoeWeight& w, int warps) {
             p.ring_at = w.integer ? 0 : few::kTableBytes;
             p.slots_at = p.ring_at + warps * kDepth * few::kStepBytes;
             p.part_at = p.slots_at + warps * 512;
         };
         const void* fn = up_fns[form_of(gate_up)];
-        if ((e = few::resident(fn, 1, dev, &fit)) != cudaSuccess) return e;
+        if ((e = few::resident(fn, kWarps * 32, 1, dev, &fit)) != cudaSuccess) return e;
         int64_t grid = chosen * (f / 8) < fit ? chosen * (f / 8) : fit;
         int warps = warps_of((chosen * (f / 8) + grid - 1) / grid * ((h + few::kStepK - 1) / few::kStepK));
         arrange(gate_up, warps);
@@ -587,7 +598,7 @@ cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, cons
 
         // down: so many output rows a CTA that the pairs' products fit
         fn = down_fns[form_of(down)];
-        if ((e = few::resident(fn, 1, dev, &fit)) != cudaSuccess) return e;
+        if ((e = few::resident(fn, kWarps * 32, 1, dev, &fit)) != cudaSuccess) return e;
         grid = h / 8 < fit ? h / 8 : fit;
         warps = warps_of(((h / 8 + grid - 1) / grid + 1) / 2 * chosen * ((f + few::kStepK - 1) / few::kStepK));
         arrange(down, warps);
