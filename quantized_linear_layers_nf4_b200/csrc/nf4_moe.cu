@@ -279,18 +279,21 @@ __device__ __forceinline__ void route(const Params& p, Route& R) {
     __syncthreads();
 }
 
-// The eight columns of an entry's products are its pairs (token, choice); those past them repeat
-// the last one, and are not used.  An expert of more than eight tokens comes again for the
+// The eight columns of an entry's products are its pairs (token, choice); those past them are not
+// used, and their lanes load no X: eight lanes (two columns) less are a pass of L1 less, and
+// L1 is what bounds these kernels.  An expert of more than eight tokens comes again for the
 // next eight: sums for sixteen at once cost registers and with them warps, on every call,
 // and few calls have such an expert.
 struct Columns {
     int idx = -1, base = 0, cnt = 0, pair = 0;  // entry of the list; its pairs; the lane's one
+    bool mine = false;                          // which is not a repetition
     __device__ __forceinline__ bool enter(const Route& R, int i, int g) {
         if (i == idx) return false;
         idx = i;
         base = R.base[i];
         cnt = R.base[i + 1] - base;
         pair = base + min(g, cnt - 1);
+        mine = g < cnt;
         return true;
     }
 };
@@ -346,10 +349,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_gate_up(const __grid_con
     auto begin = [&](int tile) {
         if (col.enter(R, (t0 + tile) / per_e, g)) x = p.xs + static_cast<int64_t>(R.pair_tok[col.pair]) * p.hp + few::x_chunk<F>(0, t) * 8;
     };
-    uint32_t q[4][4];
+    uint32_t q[4][4] = {};
     auto ahead = [&](int step) {
         const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
-        load_x<F>(q, x + to);
+        if (col.mine) load_x<F>(q, x + to);
     };
     auto mul = [&](const uint8_t* entry, int step) {
         few::multiply<F, Z, 1>(run.side, entry, run.places, run.acc, smem, bank, step, [&](int j, int, uint32_t(&v)[4]) {
@@ -451,9 +454,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_down(const __grid_consta
     auto begin = [&](int tile) {
         if (col.enter(R, tile / row_tiles, g)) x = p.act16 + static_cast<int64_t>(col.pair) * p.fp + few::x_chunk<F>(0, t) * 8;
     };
-    uint32_t q[4][4];
+    uint32_t q[4][4] = {};
     auto ahead = [&](int step) {
         const uint32_t to = static_cast<uint32_t>(step) * few::kStepK;
+        if (!col.mine) return;
         if (!conv) load_x<F>(q, x + to);
         else load_wide<F>(q, p.act32 + (x - p.act16) + to, factor[R.pair_tok[col.pair]]);
     };
