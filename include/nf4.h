@@ -519,17 +519,21 @@ nf4_status_t nf4_int4_dequantize(const nf4_int4_weight_t* w, void* out, nf4_dtyp
 
 /*
  * nf4_int4_linear -- Y = X * What^T for an integer 4-bit weight, fused like
- * nf4_linear.  For m <= 16 the products of X with the integers q - z are exact and
- * are summed in fp32, and the scale multiplies the sum of each 64 columns (each
- * group, if it is smaller): What = (q - z) s is never rounded.  For larger m the
- * weight is restored to bf16 on chip, What = bf16_round(fp32((q - z) s)), and runs on
- * the dequant-GEMM of nf4_linear.  Sums are in fp32 in an order that does not
- * depend on timing.
+ * nf4_linear.  For few tokens the products of X with the integers q - z are summed
+ * in fp32, and the scale multiplies the sum of each group's part of 128 columns:
+ * What = (q - z) s is never rounded.  (X goes through fp16 times a power of two per
+ * token and range of columns, which keeps every bit of values down to 2^-31 of the
+ * range's largest; smaller ones lose bits.)  For many tokens the weight is restored
+ * to bf16 on chip, What = bf16_round(fp32((q - z) s)), and runs on the dequant-GEMM of
+ * nf4_linear.  Up to 16 tokens are few, above 128 many; between, what is expected to
+ * be faster for m, n, k and the device decides.  Sums are in fp32 in an order that
+ * does not depend on timing.
  *   X          device, bf16 [m, k], 16-byte aligned
  *   m          rows of X (tokens), >= 1
  *   Y          device, [m, n] of y_dtype, 16-byte aligned (output)
- *   dev_status, flags  as for nf4_linear_ex (m <= 16 has no bounded waits:
- *              NF4_LINEAR_TEST_TIMEOUT is refused there with NF4_ERR_DTYPE)
+ *   dev_status, flags  as for nf4_linear_ex (the few-token kernel has no bounded waits:
+ *              NF4_LINEAR_TEST_TIMEOUT is refused for m <= 16 with NF4_ERR_DTYPE, and
+ *              takes the GEMM above)
  * Errors: as nf4_int4_dequantize; NF4_ERR_SHAPE also for m < 1, NF4_ERR_DTYPE also
  * for an unknown flag bit.
  */

@@ -140,11 +140,15 @@ class NF4Weight:
     quant_type: str = "nf4"
 
     def struct(self) -> nf4_weight_t:
-        magic = _lib.NF4_FP4_WEIGHT_MAGIC if self.quant_type == "fp4" else _lib.NF4_WEIGHT_MAGIC
-        return nf4_weight_t(magic, _lib.NF4_WEIGHT_VERSION, self.n, self.k,
-                            _lib.NF4_BLOCKSIZE, _lib.NF4_BLOCKSIZE2, self.wq.data_ptr(),
-                            self.absmax_q.data_ptr(), self.absmax_scale.data_ptr(),
-                            self.absmax_offset.data_ptr())
+        key = (self.n, self.k, self.quant_type, self.wq.data_ptr(), self.absmax_q.data_ptr(),
+               self.absmax_scale.data_ptr(), self.absmax_offset.data_ptr())
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != key:  # built once for the same tensors
+            magic = _lib.NF4_FP4_WEIGHT_MAGIC if self.quant_type == "fp4" else _lib.NF4_WEIGHT_MAGIC
+            kept = (key, nf4_weight_t(magic, _lib.NF4_WEIGHT_VERSION, self.n, self.k, _lib.NF4_BLOCKSIZE,
+                                      _lib.NF4_BLOCKSIZE2, *key[3:]))
+            self.__dict__["_kept"] = kept
+        return kept[1]
 
     def nbytes(self) -> int:
         return (self.wq.numel() + self.absmax_q.numel() + 4 * self.absmax_scale.numel())
@@ -373,23 +377,27 @@ def merge_lora(weight: NF4Weight, down: torch.Tensor, up: torch.Tensor, scale: f
 
 
 def _check_out(out: torch.Tensor, shape, dtypes, device, name: str) -> None:
-    if not out.is_cuda or out.device != device or tuple(out.shape) != shape or out.dtype not in dtypes \
-            or not out.is_contiguous():
+    if out.shape != shape or out.dtype not in dtypes or out.device != device or not out.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor on %s with one of the dtypes %s"
-                         % (name, shape, device, tuple(dtypes)))
+                         % (name, tuple(shape), device, tuple(dtypes)))
 
 
-def _launch(device: torch.device, stream, fn, where: str, *args) -> None:
-    """fn(*args, stream) on ``device``, which need not be the current one; the
+def _launch(index: int, stream, fn, where: str, *args) -> None:
+    """fn(*args, stream) on device ``index``, which need not be the current one; the
     stream is that device's current one unless given."""
-    index = device.index
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
-            return _launch(device, stream, fn, where, *args)
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    st = fn(*args, s)
+            return _launch(index, stream, fn, where, *args)
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if st != _lib.NF4_OK:
         _lib.check(st, where)
+
+
+def _group_ok(k: int, group: int) -> bool:
+    return k > 0 and group > 0 and k % 64 == 0 and (group == 32 or group % 64 == 0) and k % group == 0
+
+
+_GROUP_RULE = "k must be a multiple of 64, group 32 or a multiple of 64 that divides k"
 
 
 @dataclass(frozen=True)
@@ -406,17 +414,15 @@ class Int4Weight:
 
     def __post_init__(self):
         n, k, group = self.n, self.k, self.group
-        if n < 1 or k < 1 or group < 1 or k % 64 or (group != 32 and group % 64) or k % group:
-            raise ValueError("k must be a multiple of 64, group 32 or a multiple of 64 that divides k")
-        if not self.wq.is_cuda:
-            raise ValueError("wq must be a CUDA tensor")
-        if self.wq.numel() != n * k // 2:
-            raise ValueError("wq must hold n * k / 2 bytes")
-        dev = self.wq.device
-        _check_out(self.wq, tuple(self.wq.shape), (torch.uint8,), dev, "wq")
-        _check_out(self.scale, (k // group, n), _DTYPES, dev, "scale")
-        if self.zero is not None:
-            _check_out(self.zero, (k // group, n), (torch.uint8,), dev, "zero")
+        if n < 1 or not _group_ok(k, group):
+            raise ValueError(_GROUP_RULE)
+        wq, scale, zero = self.wq, self.scale, self.zero
+        if not wq.is_cuda or wq.dtype != torch.uint8 or wq.numel() != n * k // 2 or not wq.is_contiguous():
+            raise ValueError("wq must be a contiguous uint8 CUDA tensor of n * k / 2 bytes")
+        dev = wq.device
+        _check_out(scale, (k // group, n), _DTYPES, dev, "scale")
+        if zero is not None:
+            _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
         st = nf4_int4_weight_t(_lib.NF4_INT4_WEIGHT_MAGIC, _lib.NF4_WEIGHT_VERSION, n, k, group, _DTYPES[self.scale.dtype],
                                0, self.wq.data_ptr(), self.scale.data_ptr(),
                                None if self.zero is None else self.zero.data_ptr())
@@ -444,20 +450,22 @@ def nf4_int4_quantize(W: torch.Tensor, group: int = 128, symmetric: bool = True,
     if symmetric and zero is not None:
         raise ValueError("zero is an output of asymmetric quantization only")
     n, k = W.shape
-    if group < 1 or k % group or k % 64 or (group != 32 and group % 64):
-        raise ValueError("k must be a multiple of 64, group 32 or a multiple of 64 that divides k")
+    if not _group_ok(k, group):
+        raise ValueError(_GROUP_RULE)
     dev = W.device
     if wq is None:
         wq = torch.empty(n * k // 2, dtype=torch.uint8, device=dev)
+    else:
+        _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
     if scale is None:
         scale = torch.empty((k // group, n), dtype=scale_dtype, device=dev)
-    if zero is None and not symmetric:
-        zero = torch.empty((k // group, n), dtype=torch.uint8, device=dev)
-    _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
-    _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
+    else:
+        _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
     if zero is not None:
         _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
-    _launch(dev, stream, _lib.lib().nf4_int4_quantize, "nf4_int4_quantize", W.data_ptr(), _DTYPES[W.dtype], n, k, group,
+    elif not symmetric:
+        zero = torch.empty((k // group, n), dtype=torch.uint8, device=dev)
+    _launch(dev.index, stream, _lib.lib().nf4_int4_quantize, "nf4_int4_quantize", W.data_ptr(), _DTYPES[W.dtype], n, k, group,
             _DTYPES[scale_dtype], wq.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
     return wq, scale, zero
 
@@ -479,7 +487,7 @@ def nf4_int4_dequantize(weight: Int4Weight, dtype=torch.bfloat16, out: torch.Ten
         out = torch.empty((weight.n, weight.k), dtype=dtype, device=dev)
     else:
         _check_out(out, (weight.n, weight.k), _DTYPES, dev, "out")
-    _launch(dev, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._ref, out.data_ptr(),
+    _launch(dev.index, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._ref, out.data_ptr(),
             _DTYPES[out.dtype])
     return out
 
@@ -488,8 +496,9 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
                     dev_status: torch.Tensor | None = None, stream=None, weights_early: bool = False,
                     flags: int = 0) -> torch.Tensor:
     """Y = X @ W_hat^T for bf16 X [m, k] and an integer 4-bit weight; Y [m, n] in
-    ``dtype`` (in that of ``out``, where given).  Up to 16 tokens the weight is not
-    rounded; above, it is restored to bf16 on chip, as in nf4_linear.
+    ``dtype`` (in that of ``out``, where given).  For few tokens (up to 16, and up to
+    128 where that is faster) the weight is not rounded; for more it is restored to
+    bf16 on chip, as in nf4_linear.
     ``weights_early`` and ``flags`` as for nf4_linear."""
     _need_cuda(X, "X")
     dev = X.device
@@ -503,7 +512,7 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
     else:
         _check_out(out, (m, weight.n), _DTYPES, dev, "out")
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
-    _launch(dev, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._ref, out.data_ptr(),
+    _launch(dev.index, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._ref, out.data_ptr(),
             _DTYPES[out.dtype], None if dev_status is None else dev_status.data_ptr(), flags)
     return out
 
@@ -528,7 +537,7 @@ def nf4_moe(X: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, re
     ``workspace`` from ``moe_workspace``; it must not serve two calls at once."""
     _need_cuda(X, "X")
     _need_cuda(router, "router")
-    dev = X.device
+    index = X.get_device()
     if X.dtype != torch.bfloat16 or X.dim() != 2 or router.dtype != torch.bfloat16 or router.dim() != 2:
         raise ValueError("X and router must be 2-D bfloat16 tensors")
     m, h = X.shape
@@ -538,28 +547,28 @@ def nf4_moe(X: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, re
         raise ValueError("gate_up and down must both be NF4Weight or both be Int4Weight")
     if router.shape[1] != h or gate_up.k != h or gate_up.n != n_experts * 2 * f or down.n != n_experts * h:
         raise ValueError("shapes: X [m, h], router [E, h], gate_up [E * 2f, h], down [E * h, f]")
-    if not (router.device == gate_up.wq.device == down.wq.device == dev):
+    if router.get_device() != index or gate_up.wq.get_device() != index or down.wq.get_device() != index:
         raise ValueError("X, router and the weights must be on one device")
     if out is None:
         out = torch.empty_like(X)
     else:
-        _check_out(out, (m, h), (torch.bfloat16,), dev, "out")
+        _check_out(out, X.shape, (torch.bfloat16,), X.device, "out")
     if workspace is None:
-        workspace = moe_workspace(h, f, n_experts, top_k, dev)
+        workspace = moe_workspace(h, f, n_experts, top_k, X.device)
         if stream is not None:
             workspace.record_stream(stream)  # freed here before that stream is done with it
-    elif workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of X")
     ids = probs = None
     if return_routing:
-        ids = torch.empty((m, top_k), dtype=torch.int32, device=dev)
-        probs = torch.empty((m, top_k), dtype=torch.float32, device=dev)
+        ids = torch.empty((m, top_k), dtype=torch.int32, device=X.device)
+        probs = torch.empty((m, top_k), dtype=torch.float32, device=X.device)
     L = _lib.lib()
     if integer:
         fn, where, gu, dn = L.nf4_int4_moe, "nf4_int4_moe", gate_up._ref, down._ref
     else:
         fn, where, gu, dn = L.nf4_moe, "nf4_moe", ctypes.byref(gate_up.struct()), ctypes.byref(down.struct())
-    _launch(dev, stream, fn, where, X.data_ptr(), m, router.data_ptr(), n_experts, gu, dn, top_k, out.data_ptr(),
+    _launch(index, stream, fn, where, X.data_ptr(), m, router.data_ptr(), n_experts, gu, dn, top_k, out.data_ptr(),
             None if ids is None else ids.data_ptr(), None if probs is None else probs.data_ptr(),
             _lib.NF4_MOE_RENORMALIZE if renormalize else 0, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())

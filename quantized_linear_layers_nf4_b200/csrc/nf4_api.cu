@@ -441,18 +441,19 @@ nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* 
     if (st != NF4_OK) return st;
     if (!X || !Y) return NF4_ERR_NULL;
     if (y_dtype != NF4_F32 && y_dtype != NF4_BF16) return NF4_ERR_DTYPE;
-    const bool few = m <= nf4::kGemvMaxTokens;
-    const uint32_t allowed = few ? NF4_LINEAR_WEIGHTS_EARLY : (NF4_LINEAR_WEIGHTS_EARLY | NF4_LINEAR_TEST_TIMEOUT);
-    if ((flags & ~allowed) != 0) return NF4_ERR_DTYPE;
+    // the few-token kernel has no bounded waits to test: the flag asks for the GEMM
+    const bool test = (flags & NF4_LINEAR_TEST_TIMEOUT) != 0;
+    if ((flags & ~static_cast<uint32_t>(NF4_LINEAR_WEIGHTS_EARLY | NF4_LINEAR_TEST_TIMEOUT)) != 0 || (test && m <= nf4::kGemvMaxTokens))
+        return NF4_ERR_DTYPE;
     if (m < 1 || m > INT32_MAX / 2) return NF4_ERR_SHAPE;
     if (!aligned(X, 16) || !aligned(Y, 16) || (dev_status && !aligned(dev_status, 4))) return NF4_ERR_ALIGN;
     nf4::DeviceInfo dev;
     if ((st = device_ok(&dev)) != NF4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (few)
+    if (!test && nf4::int4_few_tokens(m, a.n, a.k, dev))
         return from_cuda(nf4::launch_int4_gemv(X, m, a, Y, y_dtype == NF4_BF16, (flags & NF4_LINEAR_WEIGHTS_EARLY) != 0, dev, s));
     return from_cuda(nf4::launch_gemm(X, m, a.wq, nullptr, nullptr, nullptr, a.n, a.k, Y, y_dtype == NF4_BF16, dev_status,
-                                      nf4::LoraArgs(), 0, (flags & NF4_LINEAR_TEST_TIMEOUT) ? nf4::kTestStall : 0u, dev, s, &a));
+                                      nf4::LoraArgs(), 0, test ? nf4::kTestStall : 0u, dev, s, &a));
 }
 
 size_t nf4_moe_workspace_bytes(int64_t h, int64_t f, int32_t n_experts, int32_t top_k) {

@@ -153,11 +153,6 @@ struct Weight {
     const float* mu;
     int codebook;
 };
-__device__ __forceinline__ uint32_t ldg_scale(const void* scale, int f32, int64_t at) {  // as fp32 bits
-    return f32 ? __ldg(reinterpret_cast<const uint32_t*>(scale) + at)
-               : static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(scale) + at)) << 16;
-}
-
 // Steps of a window, and groups (kG128: or parts of one) of a step.
 template <int F>
 constexpr int window_steps() { return F == kG128 ? 4 : (F == kG32 ? 1 : 2); }

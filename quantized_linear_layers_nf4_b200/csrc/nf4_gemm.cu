@@ -261,13 +261,20 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         // integer weights: scale and zero point of the stage's group(s), one stage ahead
         constexpr int kGroups = kInt4 == 2 ? 2 : 1;
         uint32_t gs[kGroups] = {}, gz[kGroups] = {};
-        auto fetch_sides = [&](int kt) {
+        int gleft = sides.per;
+        int64_t gat = row_c;
+        auto fetch_sides = [&](int kt) {  // kt one after the other
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
-                const int64_t at = (kInt4 == 2 ? 2 * static_cast<int64_t>(kt) + i
-                                               : static_cast<int64_t>(kt / sides.per)) * n + row_c;
-                gs[i] = few::ldg_scale(sides.scale, sides.f32, at);
-                gz[i] = sides.zero ? (__ldg(sides.zero + at) & 15u) : 8u;
+                const int64_t at = kInt4 == 2 ? (2 * static_cast<int64_t>(kt) + i) * n + row_c : gat;
+                // as loaded: anything done to it here would wait for the load
+                gs[i] = sides.f32 ? __ldg(reinterpret_cast<const uint32_t*>(sides.scale) + at)
+                                  : __ldg(reinterpret_cast<const uint16_t*>(sides.scale) + at);
+                gz[i] = sides.zero ? __ldg(sides.zero + at) : 8u;
+            }
+            if (--gleft == 0) {
+                gleft = sides.per;
+                gat += n;
             }
         };
         if (kInt4) fetch_sides(0);
@@ -280,8 +287,8 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             if (kInt4) {
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    iscale[i] = __uint_as_float(gs[i]);
-                    izero[i] = static_cast<float>(gz[i]);
+                    iscale[i] = __uint_as_float(gs[i] << (sides.f32 ? 0 : 16));
+                    izero[i] = static_cast<float>(gz[i] & 15u);
                 }
                 if (kt + 1 < nk) fetch_sides(kt + 1);
             } else if (grouped) {

@@ -1,5 +1,5 @@
-// nf4_int4_gemv.cu -- Y[t, r] = sum_c X[t, c] (q[r, c] - z) s for few tokens (m <= 16),
-// integer 4-bit weights with group scales (sm_100a).
+// nf4_int4_gemv.cu -- Y[t, r] = sum_c X[t, c] (q[r, c] - z) s for few tokens, sixteen
+// at a time, integer 4-bit weights with group scales (sm_100a).
 //
 // Bound by HBM: half a byte of code per weight.  The tensor cores (mma.sync: sixteen
 // tokens are too few for a 128-row tcgen05 tile, and the codes would have to pass
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_int4_gemv(const __grid_const
     // this CTA's k range of X
     const int first = s0 * (few::kStepK / 8);
     few::stage_x<F>(reinterpret_cast<const uint4*>(a.x) + first, a.w.k / 8, min((s0 + ns) * (few::kStepK / 8), a.w.k / 8) - first,
-                    ns * (few::kStepK / 8), a.m,                    a.x_lg, smem, a.x_stride, top, warp, lane, warps);
+                    ns * (few::kStepK / 8), a.m, a.x_lg, smem, a.x_stride, top, warp, lane, warps);
 
     const uint8_t* xb[NT][2];  // columns past m read the last token's: their sums are not stored
 #pragma unroll
@@ -185,6 +185,19 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     const size_t smem = static_cast<size_t>(a.part_at + (splits > 1 ? m * a.part_rows * 4 : 0));
     void* args[1] = {&a};
     return few::launch(fn, clusters * splits, warps * 32, smem, splits, stream, args);
+}
+
+// A pass takes 6.7 us over 1024 x 4096, 8.0 over 4096 x 4096, 12 over 11008 x 4096 and 41 over
+// 28672 x 8192, close to 6 us and 3.2 TB/s.  The GEMM, one 256 x 256 tile a CTA, takes 60 us at
+// k = 4096, 110 at 8192 and 147 at 11008 however few tokens and rows there are, until the tiles
+// are more than the SMs.  So 64 tokens over 4096 x 4096 take 33 us and 128 take 60.
+bool int4_few_tokens(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev) {
+    if (m <= kGemvMaxTokens) return true;
+    if (m > 128) return false;
+    const double pass = 6.0 + static_cast<double>(n) * static_cast<double>(k) * 0.5 / 3.2e6;
+    const int64_t tiles = (n + 255) / 256;  // m <= 256: one tile of tokens
+    const double gemm = (6.0 + 0.013 * static_cast<double>(k)) * static_cast<double>((tiles + dev.sm_count - 1) / dev.sm_count);
+    return static_cast<double>((m + kGemvMaxTokens - 1) / kGemvMaxTokens) * pass < gemm;
 }
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,

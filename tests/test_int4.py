@@ -215,7 +215,7 @@ def test_linear_few_tokens(nf4, n, k, group, zero, scale_dtype):
 def test_linear_many_tokens(nf4, n, k, group, zero, scale_dtype):
     w = _weight(nf4, n, k, group, zero, scale_dtype, n + k)
     w64 = _dense64(w)
-    for m, dtype in ((17, torch.float32), (64, torch.bfloat16), (300, torch.float32)):
+    for m, dtype in ((17, torch.float32), (64, torch.bfloat16), (100, torch.float32), (300, torch.float32)):
         x = torch.randn(m, k, device="cuda").bfloat16()
         _check(nf4.nf4_int4_linear(x, w, dtype), x, w64, rounded_weight=True)
 
