@@ -128,6 +128,20 @@ def nf4_double_quant(absmax: torch.Tensor, absmax_q: torch.Tensor | None = None,
     return absmax_q, absmax_scale, absmax_offset
 
 
+def _kept_struct(weight, key):
+    """(key, C struct, reference to it) of a weight, built again when the key (sizes and
+    data pointers) is not that of the last time."""
+    kept = weight.__dict__.get("_kept")
+    if kept is None or kept[0] != key:
+        st = weight._make(key)
+        kept = weight.__dict__["_kept"] = (key, st, ctypes.byref(st))
+    return kept
+
+
+def _without_struct(self):  # what is copied and pickled
+    return {name: v for name, v in self.__dict__.items() if name != "_kept"}
+
+
 @dataclass
 class NF4Weight:
     """A quantized [n, k] weight: device tensors plus the C struct that borrows them."""
@@ -140,15 +154,14 @@ class NF4Weight:
     quant_type: str = "nf4"
 
     def struct(self) -> nf4_weight_t:
-        key = (self.n, self.k, self.quant_type, self.wq.data_ptr(), self.absmax_q.data_ptr(),
-               self.absmax_scale.data_ptr(), self.absmax_offset.data_ptr())
-        kept = self.__dict__.get("_kept")
-        if kept is None or kept[0] != key:  # built once for the same tensors
-            magic = _lib.NF4_FP4_WEIGHT_MAGIC if self.quant_type == "fp4" else _lib.NF4_WEIGHT_MAGIC
-            kept = (key, nf4_weight_t(magic, _lib.NF4_WEIGHT_VERSION, self.n, self.k, _lib.NF4_BLOCKSIZE,
-                                      _lib.NF4_BLOCKSIZE2, *key[3:]))
-            self.__dict__["_kept"] = kept
-        return kept[1]
+        return _kept_struct(self, (self.n, self.k, self.quant_type, self.wq.data_ptr(), self.absmax_q.data_ptr(),
+                                   self.absmax_scale.data_ptr(), self.absmax_offset.data_ptr()))[1]
+
+    def _make(self, key):
+        magic = _lib.NF4_FP4_WEIGHT_MAGIC if self.quant_type == "fp4" else _lib.NF4_WEIGHT_MAGIC
+        return nf4_weight_t(magic, _lib.NF4_WEIGHT_VERSION, self.n, self.k, _lib.NF4_BLOCKSIZE, _lib.NF4_BLOCKSIZE2, *key[3:])
+
+    __getstate__ = _without_struct
 
     def nbytes(self) -> int:
         return (self.wq.numel() + self.absmax_q.numel() + 4 * self.absmax_scale.numel())
@@ -423,14 +436,18 @@ class Int4Weight:
         _check_out(scale, (k // group, n), _DTYPES, dev, "scale")
         if zero is not None:
             _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
-        st = nf4_int4_weight_t(_lib.NF4_INT4_WEIGHT_MAGIC, _lib.NF4_WEIGHT_VERSION, n, k, group, _DTYPES[self.scale.dtype],
-                               0, self.wq.data_ptr(), self.scale.data_ptr(),
-                               None if self.zero is None else self.zero.data_ptr())
-        object.__setattr__(self, "_struct", st)
-        object.__setattr__(self, "_ref", ctypes.byref(st))
+
+    def _struct_ref(self):
+        return _kept_struct(self, (self.wq.data_ptr(), self.scale.data_ptr(), None if self.zero is None else self.zero.data_ptr()))
 
     def struct(self) -> nf4_int4_weight_t:
-        return self._struct
+        return self._struct_ref()[1]
+
+    def _make(self, key):
+        return nf4_int4_weight_t(_lib.NF4_INT4_WEIGHT_MAGIC, _lib.NF4_WEIGHT_VERSION, self.n, self.k, self.group,
+                                 _DTYPES[self.scale.dtype], 0, *key)
+
+    __getstate__ = _without_struct
 
     def nbytes(self) -> int:
         return (self.wq.numel() + self.scale.numel() * self.scale.element_size() +
@@ -487,7 +504,7 @@ def nf4_int4_dequantize(weight: Int4Weight, dtype=torch.bfloat16, out: torch.Ten
         out = torch.empty((weight.n, weight.k), dtype=dtype, device=dev)
     else:
         _check_out(out, (weight.n, weight.k), _DTYPES, dev, "out")
-    _launch(dev.index, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._ref, out.data_ptr(),
+    _launch(dev.index, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._struct_ref()[2], out.data_ptr(),
             _DTYPES[out.dtype])
     return out
 
@@ -512,7 +529,7 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
     else:
         _check_out(out, (m, weight.n), _DTYPES, dev, "out")
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
-    _launch(dev.index, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._ref, out.data_ptr(),
+    _launch(dev.index, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._struct_ref()[2], out.data_ptr(),
             _DTYPES[out.dtype], None if dev_status is None else dev_status.data_ptr(), flags)
     return out
 
@@ -565,7 +582,7 @@ def nf4_moe(X: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, re
         probs = torch.empty((m, top_k), dtype=torch.float32, device=X.device)
     L = _lib.lib()
     if integer:
-        fn, where, gu, dn = L.nf4_int4_moe, "nf4_int4_moe", gate_up._ref, down._ref
+        fn, where, gu, dn = L.nf4_int4_moe, "nf4_int4_moe", gate_up._struct_ref()[2], down._struct_ref()[2]
     else:
         fn, where, gu, dn = L.nf4_moe, "nf4_moe", ctypes.byref(gate_up.struct()), ctypes.byref(down.struct())
     _launch(index, stream, fn, where, X.data_ptr(), m, router.data_ptr(), n_experts, gu, dn, top_k, out.data_ptr(),

@@ -1,7 +1,9 @@
 """Integer 4-bit weights with group scales: quantization, dequantization and the
 fused linear against plain computations (quantization step by step in fp32 as it is
 defined, everything else in 64 bits)."""
+import copy
 import ctypes
+import io
 import itertools
 
 import numpy as np
@@ -256,6 +258,36 @@ def test_streams_graph_and_repeat(nf4):
         torch.cuda.synchronize()
         assert torch.equal(ref, out)
     assert torch.equal(back, nf4.nf4_int4_dequantize(w))
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["int4", "nf4"])
+def test_weights_are_copied_and_saved(nf4, kind):
+    """A weight that was used is copied with its tensors and points to those."""
+    W = torch.randn(64, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    w, fn = (nf4.int4_quantize_weight(W, 64), nf4.nf4_int4_linear) if kind == "int4" else (nf4.quantize_weight(W), nf4.nf4_linear)
+    x = torch.randn(3, 128, device="cuda").bfloat16()
+    want = fn(x, w)
+    buf = io.BytesIO()
+    torch.save(w, buf)
+    buf.seek(0)
+    for other in (copy.deepcopy(w), copy.copy(w), torch.load(buf, weights_only=False)):
+        assert torch.equal(fn(x, other), want)
+        assert other.struct().wq == other.wq.data_ptr()
+    twin = copy.deepcopy(w)
+    twin.wq.zero_()
+    assert torch.equal(fn(x, w), want) and not torch.equal(fn(x, twin), want)
+
+
+@gpu
+def test_linear_from_few_to_many_tokens(nf4):
+    """Around every change of path the result is within that of a weight rounded to bf16."""
+    for n, k in ((64, 4096), (4096, 1024), (40000, 128)):
+        w = _weight(nf4, n, k, 128, True, torch.bfloat16, n)
+        w64 = _dense64(w)
+        for m in (16, 17, 31, 32, 33, 48, 64, 65, 96, 127, 128, 129):
+            x = torch.randn(m, k, device="cuda").bfloat16()
+            _check(nf4.nf4_int4_linear(x, w, torch.float32), x, w64, rounded_weight=True)
 
 
 @gpu

@@ -153,7 +153,8 @@ def _check(nf4, x, layer, top, renorm, **kw):
 
 
 CASES = [(1, 4, 1, 64, 64), (1, 1, 1, 128, 64), (3, 3, 3, 64, 192), (7, 40, 6, 448, 128), (8, 8, 2, 1024, 704), (9, 8, 2, 512, 320),
-         (16, 64, 8, 320, 64), (16, 2, 1, 256, 1408), (5, 512, 16, 128, 64), (16, 300, 16, 64, 64), (17, 4, 2, 192, 128), (35, 10, 4, 128, 192)]
+         (16, 64, 8, 320, 64), (16, 2, 1, 256, 1408), (5, 512, 16, 128, 64), (16, 300, 16, 64, 64), (17, 4, 2, 192, 128), (35, 10, 4, 128, 192),
+         (16, 1, 1, 192, 64), (16, 3, 3, 128, 320), (13, 20, 16, 64, 128), (2, 2, 2, 65536, 64), (1, 1, 1, 64, 65536)]
 
 
 @gpu
@@ -178,6 +179,14 @@ def test_range(nf4, fmt, scale):
     x[5] = 0
     y = _check(nf4, x.bfloat16(), layer, 2, True)
     assert torch.all(y[5] == 0)
+
+
+@gpu
+def test_groups_of_the_two_weights_differ(nf4):
+    a, b = _layer(nf4, 6, 384, 256, "int4_32", seed=1), _layer(nf4, 6, 384, 256, "int4_row", seed=2)
+    x = torch.randn(9, 384, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7)).bfloat16()
+    _check(nf4, x, (a[0], a[1], b[2]), 3, True)
+    _check(nf4, x, (a[0], b[1], a[2]), 3, False)
 
 
 @gpu
