@@ -75,10 +75,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
+// A word's eight integer codes as bf16((q - z) s), pairs in k order.  A nibble in the low bits
+// of 128's mantissa is 128 + q; less z2 = 128 + z it is q - z, exact, and the product of that
+// with a bf16 scale (s2: twice) is exact before its one rounding, so these are the values
+// that nf4_int4_dequantize writes.
+__device__ __forceinline__ void int4_bf16(uint32_t w, uint32_t z2, uint32_t s2, uint32_t (&o)[4]) {
+    const uint32_t v = w >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = prmt(v, w, 0x4400u + 0x1111u * i);  // byte i of v, of w, twice each
+        uint32_t d;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(few::and_or(p, 0x000f000fu, 0x43004300u)), "r"(z2));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(d), "r"(s2));
+    }
+}
+
 // kInt4: the codes are integers with group scales instead of codebook levels --
-// 1: groups of whole 64-k stages, 2: groups of 32, two tables per stage.  The
-// 16-entry table of a group is bf16(fp32((j - z) s)), what nf4_int4_dequantize
-// writes; everything else is the same.
+// 1: groups of whole 64-k stages, 2: groups of 32.  With bf16 scales two codes at a time take
+// one permute, one logic and two packed bf16 operations (half the integer pipe's work of the
+// table, which bounds the kernel); with fp32 scales a group has a 16-entry
+// table bf16(fp32((j - z) s)) as a codebook's block has.  Everything else is the same.
 template <bool kBf16Out, bool kLora, int kInt4>
 __global__ void __launch_bounds__(kThreads, 1)
 k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -283,12 +299,12 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             const int sb = kt % kStagesB;
             int q = 0;
             float sc = 0.0f;
-            float iscale[kGroups], izero[kGroups];
+            uint32_t iscale[kGroups], izero[kGroups];
             if (kInt4) {
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    iscale[i] = __uint_as_float(gs[i] << (sides.f32 ? 0 : 16));
-                    izero[i] = static_cast<float>(gz[i] & 15u);
+                    iscale[i] = gs[i];
+                    izero[i] = gz[i] & 15u;
                 }
                 if (kt + 1 < nk) fetch_sides(kt + 1);
             } else if (grouped) {
@@ -316,13 +332,15 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             if (lane == 0) mbar_arrive(&empty_p[sp]);
             Planes P;
             auto int4_planes = [&](int i) {
-                const uint64_t off = dup_f32x2(-izero[i]);
+                const uint64_t off = dup_f32x2(-static_cast<float>(izero[i]));
                 uint64_t lev[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lev[j]) : "l"(cpair[j]), "l"(off));
-                build_planes(lev, iscale[i], P);
+                build_planes(lev, __uint_as_float(iscale[i]), P);
             };
-            if (kInt4) int4_planes(0);
+            const bool pairs = kInt4 && !sides.f32;
+            if (pairs) {
+            } else if (kInt4) int4_planes(0);
             else build_planes(cpair, absmax_hat(q, sc, mu), P);
             if (kt >= kStagesB && !__all_sync(kFull, mbar_wait_n(&empty_b[sb], ((kt / kStagesB) - 1) & 1, lim))) {
                 timed_out = true;
@@ -330,14 +348,29 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             }
             const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
             const uint32_t bst = brow + sb * kBBytes;
+            if (pairs) {
+                uint32_t z2[kGroups], s2[kGroups];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (kInt4 == 2 && c == 4) int4_planes(1);
-                const uint32_t x = w[c] ^ 0x88888888u;
-                uint32_t o0, o1, o2, o3;
-                decode4(w[c], x, P, o0, o1);
-                decode4(w[c] >> 16, x >> 16, P, o2, o3);
-                sts128(bst + ((c ^ swz) << 4), o0, o1, o2, o3);
+                for (int i = 0; i < kGroups; ++i) {
+                    z2[i] = izero[i] * 0x10001u + 0x43004300u;
+                    s2[i] = iscale[i] * 0x10001u;
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[4];
+                    int4_bf16(w[c], z2[kGroups * c / 8], s2[kGroups * c / 8], o);
+                    sts128(bst + ((c ^ swz) << 4), o[0], o[1], o[2], o[3]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if (kInt4 == 2 && c == 4) int4_planes(1);
+                    const uint32_t x = w[c] ^ 0x88888888u;
+                    uint32_t o0, o1, o2, o3;
+                    decode4(w[c], x, P, o0, o1);
+                    decode4(w[c] >> 16, x >> 16, P, o2, o3);
+                    sts128(bst + ((c ^ swz) << 4), o0, o1, o2, o3);
+                }
             }
             fence_proxy_async_shared();  // generic-proxy writes -> tensor-core reads
             __syncwarp();
