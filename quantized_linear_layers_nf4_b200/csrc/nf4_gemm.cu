@@ -54,6 +54,9 @@ constexpr int kBBytes = kBN * kBK * 2;  // 32768
 constexpr int kPBytes = kBN * kBK / 2;  // 8192
 constexpr int kDequantWarps = 8;
 constexpr int kThreads = 32 * (4 + kDequantWarps);
+// A decoding warp spends more of a stage waiting than working: two teams of them take turns for integer
+// codes, whose decoding needs few enough registers.
+constexpr int threads_of(int integer) { return integer ? kThreads + 32 * kDequantWarps : kThreads; }
 constexpr uint32_t kTmemCols = 512;
 constexpr int kOffB = kStagesA * kABytes;
 constexpr int kOffP = kOffB + kStagesB * kBBytes;
@@ -96,7 +99,7 @@ __device__ __forceinline__ void int4_bf16(uint32_t w, uint32_t z2, uint32_t s2, 
 // table, which bounds the kernel); with fp32 scales a group has a 16-entry
 // table bf16(fp32((j - z) s)) as a codebook's block has.  Everything else is the same.
 template <bool kBf16Out, bool kLora, int kInt4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(kInt4), 1)
 k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
            const int8_t* __restrict__ absmax_q, const float* __restrict__ absmax_scale,
            const float* __restrict__ mu_ptr, int64_t m, int64_t n, int64_t k, void* __restrict__ Y,
@@ -104,7 +107,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
            const __nv_bfloat16* __restrict__ lora_up, int lora_r, int lora_tc,
            const __grid_constant__ CUtensorMap tm_thi, const __grid_constant__ CUtensorMap tm_tlo,
            const __grid_constant__ CUtensorMap tm_up, int codebook, uint32_t lim, int stall,
-           const few::Weight sides) {
+           const few::Weight sides, int tile_n, int x_rows) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -120,10 +123,12 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
     uint64_t* mma_done = lora_full + 1;   // every MMA issued so far has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = few::warp_index();
     const int lane = threadIdx.x & 31;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kBN;
+    const int bn = kInt4 ? tile_n : kBN;  // weight rows of the tile
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * bn;
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kBM;
+    const int halves = kInt4 && m - m0 <= 128 ? 1 : 2;  // of the token tile that hold any
     const int nk = static_cast<int>(k / kBK);
     const uint32_t sbase = smem_u32(smem);
 
@@ -164,7 +169,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                     timed_out = true;
                     break;
                 }
-                mbar_arrive_expect_tx(&full_a[s], kABytes);
+                mbar_arrive_expect_tx(&full_a[s], kInt4 ? x_rows * kBK * 2 : kABytes);
                 tma_load_2d(smem + s * kABytes, &tm_x, kt * kBK, static_cast<int32_t>(m0), &full_a[s]);
                 issued = kt + 1;
             }
@@ -183,7 +188,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                     timed_out = true;
                     break;
                 }
-                mbar_arrive_expect_tx(&full_p[s], kPBytes);
+                mbar_arrive_expect_tx(&full_p[s], bn * kBK / 2);
                 tma_load_2d(smem + kOffP + s * kPBytes, &tm_w, kt * (kBK / 2), static_cast<int32_t>(n0),
                             &full_p[s]);
                 issued = kt + 1;
@@ -194,26 +199,34 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ----------------------------
-        if (lane == 0) {
-            for (int kt = 0; kt < nk; ++kt) {
-                const int sa = kt % kStagesA;
-                const int sb = kt % kStagesB;
-                if (!mbar_wait_n(&full_a[sa], (kt / kStagesA) & 1, lim) || !mbar_wait_n(&full_b[sb], (kt / kStagesB) & 1, lim)) {
-                    timed_out = true;
-                    break;
+        // The whole warp walks the stages, so that the descriptors stay in uniform registers, and
+        // one thread issues: by a branch of one lane alone each MMA took 77 cycles to issue.
+        const bool leader = elect_one();
+        const uint32_t idesc = kInt4 ? (kIdesc & ~(0x3fu << 17)) | static_cast<uint32_t>(bn >> 3) << 17 : kIdesc;
+        for (int kt = 0; kt < nk; ++kt) {
+            const int sa = kt % kStagesA;
+            const int sb = kt % kStagesB;
+            if (!__all_sync(kFull, mbar_wait_n(&full_a[sa], (kt / kStagesA) & 1, lim) &&
+                                       mbar_wait_n(&full_b[sb], (kt / kStagesB) & 1, lim))) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t a_desc = smem_desc_sw128(sbase + sa * kABytes), b_desc = smem_desc_sw128(sbase + kOffB + sb * kBBytes);
+            if (leader) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (kInt4 && h == halves) break;
+#pragma unroll
+                    for (int j = 0; j < kBK / 16; ++j)  // a descriptor counts 16 bytes
+                        tc_mma_bf16(tmem + h * 256, a_desc + h * (128 * 128 / 16) + 2 * j, b_desc + 2 * j, idesc, (kt > 0 || j > 0) ? 1u : 0u);
                 }
-                tc_fence_after();
-                const uint32_t a_addr = sbase + sa * kABytes;
-                const uint32_t b_addr = sbase + kOffB + sb * kBBytes;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j)
-                        tc_mma_bf16(tmem + h * 256, smem_desc_sw128(a_addr + h * (128 * 128) + 32 * j),
-                                    smem_desc_sw128(b_addr + 32 * j), kIdesc, (kt > 0 || j > 0) ? 1u : 0u);
                 tc_commit(&empty_a[sa]);
                 tc_commit(&empty_b[sb]);
             }
+            __syncwarp();
+        }
+        if (leader) {
             if (kLora && lora_tc && !timed_out) {
                 // Low-rank term on the tensor cores: Y += t_hi up^T + t_lo up^T, with
                 // t = t_hi + t_lo (two bf16 halves) and up as the B operand, in K
@@ -250,7 +263,13 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         }
     } else if (warp >= 4) {
         // ------------------------ dequantize, then epilogue --------------------
-        const int t = threadIdx.x - 128;  // weight row of the tile
+        // weight row of the tile; where that has few, two, four or eight threads share one
+        constexpr int kTeams = kInt4 ? 2 : 1;  // of decoding warps, which take stages in turn
+        const int share = (kInt4 == 0 || bn > 128) ? 0 : (bn > 64 ? 1 : (bn > 32 ? 2 : 3));
+        const int team = kInt4 ? (warp - 4) / kDequantWarps : 0, local = threadIdx.x - 128 - team * 32 * kDequantWarps;
+        const int part = kInt4 ? local / bn : 0;  // one in a warp
+        const int t = local - part * bn;
+        const bool busy = part >> share == 0;
         const int64_t row_c = (n0 + t < n) ? n0 + t : n - 1;  // rows past n: computed, never stored
         const int64_t kblocks = k / 64;
         const float mu = kInt4 ? 0.0f : __ldg(mu_ptr);
@@ -274,27 +293,29 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             qw_next = __ldg(reinterpret_cast<const uint32_t*>(absmax_q + rbase));
             s_next = __ldg(absmax_scale + (rbase >> 8));
         }
-        // integer weights: scale and zero point of the stage's group(s), one stage ahead
+        // integer weights: scale and zero point of the team's next stage
         constexpr int kGroups = kInt4 == 2 ? 2 : 1;
         uint32_t gs[kGroups] = {}, gz[kGroups] = {};
         int gleft = sides.per;
         int64_t gat = row_c;
-        auto fetch_sides = [&](int kt) {  // kt one after the other
+        auto later = [&](int stages) {
+            if (kInt4 == 2) gat += 2 * stages * n;
+            else for (gleft -= stages; gleft <= 0; gleft += sides.per) gat += n;
+        };
+        auto fetch_sides = [&] {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
-                const int64_t at = kInt4 == 2 ? (2 * static_cast<int64_t>(kt) + i) * n + row_c : gat;
                 // as loaded: anything done to it here would wait for the load
-                gs[i] = sides.f32 ? __ldg(reinterpret_cast<const uint32_t*>(sides.scale) + at)
-                                  : __ldg(reinterpret_cast<const uint16_t*>(sides.scale) + at);
-                gz[i] = sides.zero ? __ldg(sides.zero + at) : 8u;
-            }
-            if (--gleft == 0) {
-                gleft = sides.per;
-                gat += n;
+                gs[i] = sides.f32 ? __ldg(reinterpret_cast<const uint32_t*>(sides.scale) + gat + i * n)
+                                  : __ldg(reinterpret_cast<const uint16_t*>(sides.scale) + gat + i * n);
+                gz[i] = sides.zero ? __ldg(sides.zero + gat + i * n) : 8u;
             }
         };
-        if (kInt4) fetch_sides(0);
-        for (int kt = 0; kt < nk; ++kt) {
+        if (kInt4) {
+            if (team) later(team);
+            if (team < nk) fetch_sides();
+        }
+        for (int kt = team; kt < nk; kt += kTeams) {
             const int sp = kt % kStagesP;
             const int sb = kt % kStagesB;
             int q = 0;
@@ -306,7 +327,10 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                     iscale[i] = gs[i];
                     izero[i] = gz[i] & 15u;
                 }
-                if (kt + 1 < nk) fetch_sides(kt + 1);
+                if (kt + kTeams < nk) {
+                    later(kTeams);
+                    fetch_sides();
+                }
             } else if (grouped) {
                 if ((kt & 3) == 0) {
                     qw_cur = qw_next;
@@ -326,10 +350,11 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                 timed_out = true;
                 break;
             }
-            const uint4 r0 = lds128(prow + sp * kPBytes);
-            const uint4 r1 = lds128(prow + sp * kPBytes + 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty_p[sp]);
+            uint4 r0 = {}, r1 = {};
+            if (busy) {
+                r0 = lds128(prow + sp * kPBytes);
+                r1 = lds128(prow + sp * kPBytes + 16);
+            }
             Planes P;
             auto int4_planes = [&](int i) {
                 const uint64_t off = dup_f32x2(-static_cast<float>(izero[i]));
@@ -348,7 +373,8 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             }
             const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
             const uint32_t bst = brow + sb * kBBytes;
-            if (pairs) {
+            if (!busy) {
+            } else if (pairs) {
                 uint32_t z2[kGroups], s2[kGroups];
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
@@ -357,6 +383,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
+                    if ((c << share) >> 3 != part) continue;
                     uint32_t o[4];
                     int4_bf16(w[c], z2[kGroups * c / 8], s2[kGroups * c / 8], o);
                     sts128(bst + ((c ^ swz) << 4), o[0], o[1], o[2], o[3]);
@@ -365,6 +392,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     if (kInt4 == 2 && c == 4) int4_planes(1);
+                    if (kInt4 && (c << share) >> 3 != part) continue;
                     const uint32_t x = w[c] ^ 0x88888888u;
                     uint32_t o0, o1, o2, o3;
                     decode4(w[c], x, P, o0, o1);
@@ -374,19 +402,21 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             }
             fence_proxy_async_shared();  // generic-proxy writes -> tensor-core reads
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full_b[sb]);
+            if (lane == 0) {
+                mbar_arrive(&full_b[sb]);
+                mbar_arrive(&empty_p[sp]);  // here, where the codes were used: before that, a load may still be under way
+            }
         }
         // epilogue: accumulators -> Y
         const bool ok = !timed_out && __all_sync(kFull, mbar_wait_n(acc_ready, 0, lim));
         if (!ok) timed_out = true;
         tc_fence_after();
-        const int wd = warp - 4;
-        const int half = wd >> 2;
+        const int half = (warp - 4) >> 2 & 1;
         const int quarter = warp & 3;  // tensor-memory lanes this warp may access
         const int64_t tok = m0 + half * 128 + quarter * 32 + lane;
         const bool vec = kBf16Out ? (n % 8 == 0) : (n % 4 == 0);
 #pragma unroll 1
-        for (int cc = 0; cc < kBN / 32; ++cc) {
+        for (int cc = team; cc < bn / 32; cc += kTeams) {
             uint32_t r[32];
             if (ok) tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 256 + cc * 32, r);
             const int64_t col0 = n0 + cc * 32;
@@ -709,6 +739,24 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Weight rows of a tile for integer codes: a stage takes a time that goes about as 350 + rows,
+// since most of it is the decoding warps' latency, and the waves of tiles over the SMs go in
+// whole numbers.  512 x 11008x4096 takes 48 us with 160 rows (69 x 2 tiles) and 59 with 256
+// (43 x 2); 256 x 4096x4096 32 us with 32 rows and 53 with 256.
+int tile_rows(int64_t m, int64_t n, int sms) {
+    int best = kBN;
+    int64_t least = INT64_MAX;
+    for (int rows = kBN; rows >= 32; rows -= 32) {
+        const int64_t tiles = (n + rows - 1) / rows * ((m + kBM - 1) / kBM);
+        const int64_t cost = (tiles + sms - 1) / sms * (350 + rows);
+        if (cost < least) {
+            least = cost;
+            best = rows;
+        }
+    }
+    return best;
+}
+
 }  // namespace gemm
 
 cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_t* absmax_q,
@@ -746,15 +794,17 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
             attr_set[dev.device][vi] = true;
         }
     }
+    const int x_rows = w4 && m <= 128 ? 128 : gemm::kBM;
+    const int bn = w4 ? gemm::tile_rows(m, n, dev.sm_count) : gemm::kBN;
     CUtensorMap tm_x, tm_w;
     cudaError_t e = tmap_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, static_cast<uint64_t>(k),
-                            static_cast<uint64_t>(m), static_cast<uint64_t>(k * 2), gemm::kBK, gemm::kBM,
+                            static_cast<uint64_t>(m), static_cast<uint64_t>(k * 2), gemm::kBK, x_rows,
                             CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     e = tmap_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, static_cast<uint64_t>(k / 2), static_cast<uint64_t>(n),
-                static_cast<uint64_t>(k / 2), gemm::kBK / 2, gemm::kBN, CU_TENSOR_MAP_SWIZZLE_NONE);
+                static_cast<uint64_t>(k / 2), gemm::kBK / 2, bn, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((n + gemm::kBN - 1) / gemm::kBN),
+    const dim3 grid(static_cast<unsigned>((n + bn - 1) / bn),
                     static_cast<unsigned>((m + gemm::kBM - 1) / gemm::kBM));
     // the low-rank term on the tensor cores needs 16-byte rows of t_hi / t_lo / up (r % 8 == 0)
     int lora_tc = 0;
@@ -773,10 +823,10 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         lora_tc = 1;
     }
 #define NF4_GEMM_LAUNCH(B, L, F)                                                                               \
-    gemm::k_nf4_gemm<B, L, F><<<grid, gemm::kThreads, gemm::kSmemBytes, stream>>>(                              \
+    gemm::k_nf4_gemm<B, L, F><<<grid, gemm::threads_of(F), gemm::kSmemBytes, stream>>>(                              \
         tm_x, tm_w, absmax_q, absmax_scale, absmax_offset, m, n, k, Y, dev_status, lora.t, lora.up, lora.r,  \
         lora_tc, tm_thi, tm_tlo, tm_up, codebook, (test_flags & kTestStall) ? 64u : kWaitLimit,            \
-        (test_flags & kTestStall) ? 1 : 0, sides)
+        (test_flags & kTestStall) ? 1 : 0, sides, bn, x_rows)
     switch (vi) {
         case 0: NF4_GEMM_LAUNCH(false, false, 0); break;
         case 1: NF4_GEMM_LAUNCH(true, false, 0); break;
