@@ -525,9 +525,9 @@ nf4_status_t nf4_int4_dequantize(const nf4_int4_weight_t* w, void* out, nf4_dtyp
  * token and range of columns, which keeps every bit of values down to 2^-31 of the
  * range's largest; smaller ones lose bits.)  For many tokens the weight is restored
  * to bf16 on chip, What = bf16_round(fp32((q - z) s)), and runs on the dequant-GEMM of
- * nf4_linear.  Up to 16 tokens are few, above 128 many; between, what is expected to
- * be faster for m, n, k and the device decides.  Sums are in fp32 in an order that
- * does not depend on timing.
+ * nf4_linear.  Up to 16 tokens are few; above, the path that is expected to be faster
+ * for m, n, k and the device's number of SMs.  Sums are in fp32 in an order that does
+ * not depend on timing.
  *   X          device, bf16 [m, k], 16-byte aligned
  *   m          rows of X (tokens), >= 1
  *   Y          device, [m, n] of y_dtype, 16-byte aligned (output)

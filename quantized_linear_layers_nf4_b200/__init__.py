@@ -513,9 +513,9 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
                     dev_status: torch.Tensor | None = None, stream=None, weights_early: bool = False,
                     flags: int = 0) -> torch.Tensor:
     """Y = X @ W_hat^T for bf16 X [m, k] and an integer 4-bit weight; Y [m, n] in
-    ``dtype`` (in that of ``out``, where given).  For few tokens (up to 16, and up to
-    128 where that is faster) the weight is not rounded; for more it is restored to
-    bf16 on chip, as in nf4_linear.
+    ``dtype`` (in that of ``out``, where given).  For few tokens (up to 16, and more
+    where that is faster) the weight is not rounded; otherwise it is restored to bf16
+    on chip, as in nf4_linear.
     ``weights_early`` and ``flags`` as for nf4_linear."""
     _need_cuda(X, "X")
     dev = X.device

@@ -742,15 +742,15 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
 // Weight rows of a tile for integer codes: a stage takes a time that goes about as 350 + rows,
 // since most of it is the decoding warps' latency, and the waves of tiles over the SMs go in
 // whole numbers.  512 x 11008x4096 takes 48 us with 160 rows (69 x 2 tiles) and 59 with 256
-// (43 x 2); 256 x 4096x4096 32 us with 32 rows and 53 with 256.
-int tile_rows(int64_t m, int64_t n, int sms) {
+// (43 x 2); 256 x 4096x4096 32 us with 32 rows and 53 with 256.  `cost`: of all stages of one k.
+int tile_rows(int64_t m, int64_t n, int sms, int64_t* cost) {
     int best = kBN;
-    int64_t least = INT64_MAX;
+    *cost = INT64_MAX;
     for (int rows = kBN; rows >= 32; rows -= 32) {
         const int64_t tiles = (n + rows - 1) / rows * ((m + kBM - 1) / kBM);
-        const int64_t cost = (tiles + sms - 1) / sms * (350 + rows);
-        if (cost < least) {
-            least = cost;
+        const int64_t c = (tiles + sms - 1) / sms * (350 + rows);
+        if (c < *cost) {
+            *cost = c;
             best = rows;
         }
     }
@@ -795,7 +795,8 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         }
     }
     const int x_rows = w4 && m <= 128 ? 128 : gemm::kBM;
-    const int bn = w4 ? gemm::tile_rows(m, n, dev.sm_count) : gemm::kBN;
+    int64_t cost = 0;
+    const int bn = w4 ? gemm::tile_rows(m, n, dev.sm_count, &cost) : gemm::kBN;
     CUtensorMap tm_x, tm_w;
     cudaError_t e = tmap_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, static_cast<uint64_t>(k),
                             static_cast<uint64_t>(m), static_cast<uint64_t>(k * 2), gemm::kBK, x_rows,
@@ -839,6 +840,12 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
     }
 #undef NF4_GEMM_LAUNCH
     return cudaGetLastError();
+}
+
+double int4_gemm_us(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev) {
+    int64_t cost = 0;
+    gemm::tile_rows(m, n, dev.sm_count, &cost);
+    return 5.0 + 0.95e-3 * static_cast<double>(cost) * static_cast<double>(k / gemm::kBK);
 }
 
 cudaError_t launch_gemm_dx(const void* dY, int64_t m, const uint8_t* wq, const int8_t* absmax_q,

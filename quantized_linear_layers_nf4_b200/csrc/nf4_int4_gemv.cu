@@ -187,25 +187,27 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     return few::launch(fn, clusters * splits, warps * 32, smem, splits, stream, args);
 }
 
-// A pass takes 6.7 us over 1024 x 4096, 8.0 over 4096 x 4096, 12 over 11008 x 4096 and 41 over
-// 28672 x 8192, close to 6 us and 3.2 TB/s.  The GEMM, one 256 x 256 tile a CTA, takes 60 us at
-// k = 4096, 110 at 8192 and 147 at 11008 however few tokens and rows there are, until the tiles
-// are more than the SMs.  So 64 tokens over 4096 x 4096 take 33 us and 128 take 60.
-bool int4_few_tokens(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev) {
+// Tokens of a pass: so many that an eighth of their X leaves room for 16 KB of sums (all sixteen
+// up to k = 26624, eight to 47104, then four).
+static int64_t tokens_of_pass(int64_t m, const Int4Args& w) {
+    int64_t most = kGemvMaxTokens;
+    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w), int4::kWarps).left < 16 * 1024) most /= 2;
+    return most;
+}
+
+// A pass takes 6.7 us over 1024 x 4096, 8.0 over 4096 x 4096, 12 over 11008 x 4096, 41 over
+// 28672 x 8192 and 14 over 512 x 65536: 6 us, 3.2 TB/s and X.  The GEMM (int4_gemm_us) takes 27 us
+// over 4096 x 4096, 32 over 11008 x 4096 and 78 over 28672 x 8192 for any number of tokens up to 128.
+bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev) {
     if (m <= kGemvMaxTokens) return true;
-    if (m > 128) return false;
-    const double pass = 6.0 + static_cast<double>(n) * static_cast<double>(k) * 0.5 / 3.2e6;
-    const int64_t tiles = (n + 255) / 256;  // m <= 256: one tile of tokens
-    const double gemm = (6.0 + 0.013 * static_cast<double>(k)) * static_cast<double>((tiles + dev.sm_count - 1) / dev.sm_count);
-    return static_cast<double>((m + kGemvMaxTokens - 1) / kGemvMaxTokens) * pass < gemm;
+    const double k = static_cast<double>(w.k), pass = 6.0 + static_cast<double>(w.n) * k * 0.5 / 3.2e6 + k * 5e-5;
+    const int64_t most = tokens_of_pass(m, w);
+    return static_cast<double>((m + most - 1) / most) * pass < int4_gemm_us(m, w.n, w.k, dev);
 }
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,
                              cudaStream_t stream) {
-    // so many tokens at a time that an eighth of their X leaves room for 16 KB of sums (all
-    // sixteen up to k = 26624, eight to 47104, then four)
-    int64_t most = kGemvMaxTokens;
-    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w), int4::kWarps).left < 16 * 1024) most /= 2;
+    const int64_t most = tokens_of_pass(m, w);
     for (int64_t t = 0; t < m; t += most) {
         const cudaError_t e = launch_int4_gemv_pass(static_cast<const char*>(X) + t * w.k * 2, m - t < most ? m - t : most, w,
                                                     static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, dev, stream);
