@@ -670,8 +670,6 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
             }
             const uint4 r0 = lds128(prow + sp * kPBytes + ((((2 * cb) ^ static_cast<int>(swz))) << 4));
             const uint4 r1 = lds128(prow + sp * kPBytes + ((((2 * cb + 1) ^ static_cast<int>(swz))) << 4));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty_p[sp]);
             Planes P;
             build_planes(cpair, absmax_hat(q, sc, mu), P);
             if (rt >= kStagesB && !__all_sync(kFull, mbar_wait(&empty_b[sb], ((rt / kStagesB) - 1) & 1))) {
@@ -690,7 +688,10 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
             }
             fence_proxy_async_shared();  // generic-proxy writes -> tensor-core reads
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full_b[sb]);
+            if (lane == 0) {
+                mbar_arrive(&full_b[sb]);
+                mbar_arrive(&empty_p[sp]);  // as in k_nf4_gemm
+            }
         }
         // epilogue: accumulators -> dX
         const bool ok = !timed_out && __all_sync(kFull, mbar_wait(acc_ready, 0));
