@@ -156,6 +156,10 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (kInt4) {  // a programmatic dependent: nothing of the preceding kernels' is touched before this
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
 
     bool timed_out = false;
     if (warp == 0) {
@@ -824,11 +828,20 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         if (e != cudaSuccess) return e;
         lora_tc = 1;
     }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = w4 ? 1 : 0;
 #define NF4_GEMM_LAUNCH(B, L, F)                                                                               \
-    gemm::k_nf4_gemm<B, L, F><<<grid, gemm::threads_of(F), gemm::kSmemBytes, stream>>>(                              \
-        tm_x, tm_w, absmax_q, absmax_scale, absmax_offset, m, n, k, Y, dev_status, lora.t, lora.up, lora.r,  \
-        lora_tc, tm_thi, tm_tlo, tm_up, codebook, (test_flags & kTestStall) ? 64u : kWaitLimit,            \
-        (test_flags & kTestStall) ? 1 : 0, sides, bn, x_rows)
+    cfg.blockDim = dim3(gemm::threads_of(F));                                                                  \
+    cfg.dynamicSmemBytes = gemm::kSmemBytes;                                                                   \
+    e = cudaLaunchKernelEx(&cfg, gemm::k_nf4_gemm<B, L, F>, tm_x, tm_w, absmax_q, absmax_scale, absmax_offset, m, n, k, Y, \
+                           dev_status, lora.t, lora.up, lora.r, lora_tc, tm_thi, tm_tlo, tm_up, codebook,       \
+                           (test_flags & kTestStall) ? 64u : kWaitLimit, (test_flags & kTestStall) ? 1 : 0, sides, bn, x_rows)
     switch (vi) {
         case 0: NF4_GEMM_LAUNCH(false, false, 0); break;
         case 1: NF4_GEMM_LAUNCH(true, false, 0); break;
@@ -840,7 +853,7 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         default: NF4_GEMM_LAUNCH(true, false, 2); break;
     }
 #undef NF4_GEMM_LAUNCH
-    return cudaGetLastError();
+    return e;
 }
 
 double int4_gemm_us(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev) {
