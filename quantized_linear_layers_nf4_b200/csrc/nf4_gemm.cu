@@ -54,6 +54,7 @@ constexpr int kBBytes = kBN * kBK * 2;  // 32768
 constexpr int kPBytes = kBN * kBK / 2;  // 8192
 constexpr int kDequantWarps = 8;
 constexpr int kThreads = 32 * (4 + kDequantWarps);
+constexpr int kInt4F32 = 4;
 // A decoding warp spends more of a stage waiting than working: two teams of them take turns for integer
 // codes, whose decoding needs few enough registers.
 constexpr int threads_of(int integer) { return integer ? kThreads + 32 * kDequantWarps : kThreads; }
@@ -94,7 +95,7 @@ __device__ __forceinline__ void int4_bf16(uint32_t w, uint32_t z2, uint32_t s2, 
 }
 
 // kInt4: the codes are integers with group scales instead of codebook levels --
-// 1: groups of whole 64-k stages, 2: groups of 32.  With bf16 scales two codes at a time take
+// 1: groups of whole 64-k stages, 2: groups of 32; and kInt4F32.  With bf16 scales two codes at a time take
 // one permute, one logic and two packed bf16 operations (half the integer pipe's work of the
 // table, which bounds the kernel); with fp32 scales a group has a 16-entry
 // table bf16(fp32((j - z) s)) as a codebook's block has.  Everything else is the same.
@@ -298,21 +299,33 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             s_next = __ldg(absmax_scale + (rbase >> 8));
         }
         // integer weights: scale and zero point of the team's next stage
-        constexpr int kGroups = kInt4 == 2 ? 2 : 1;
+        constexpr bool kF32 = (kInt4 & kInt4F32) != 0;
+        constexpr int kGroups = (kInt4 & 3) == 2 ? 2 : 1, kScale = kF32 ? 4 : 2;
         uint32_t gs[kGroups] = {}, gz[kGroups] = {};
-        int gleft = sides.per;
-        int64_t gat = row_c;
+        const uint8_t* s_at = reinterpret_cast<const uint8_t*>(sides.scale) + kScale * row_c;
+        const uint8_t* z_at = sides.zero ? sides.zero + row_c : nullptr;
+        const int64_t z_row = sides.zero ? n : 0;
+        int gleft = sides.per;  // stages to the next group
         auto later = [&](int stages) {
-            if (kInt4 == 2) gat += 2 * stages * n;
-            else for (gleft -= stages; gleft <= 0; gleft += sides.per) gat += n;
+            if (kGroups == 2) {
+                s_at += 2 * stages * kScale * n;
+                z_at += 2 * stages * z_row;
+                return;
+            }
+            gleft -= stages;
+            while (gleft <= 0) {
+                gleft += sides.per;
+                s_at += kScale * n;
+                z_at += z_row;
+            }
         };
         auto fetch_sides = [&] {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 // as loaded: anything done to it here would wait for the load
-                gs[i] = sides.f32 ? __ldg(reinterpret_cast<const uint32_t*>(sides.scale) + gat + i * n)
-                                  : __ldg(reinterpret_cast<const uint16_t*>(sides.scale) + gat + i * n);
-                gz[i] = sides.zero ? __ldg(sides.zero + gat + i * n) : 8u;
+                gs[i] = kF32 ? __ldg(reinterpret_cast<const uint32_t*>(s_at + i * kScale * n))
+                             : __ldg(reinterpret_cast<const uint16_t*>(s_at + i * kScale * n));
+                gz[i] = z_at ? __ldg(z_at + i * z_row) : 8u;
             }
         };
         if (kInt4) {
@@ -367,7 +380,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                 for (int j = 0; j < 8; ++j) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lev[j]) : "l"(cpair[j]), "l"(off));
                 build_planes(lev, __uint_as_float(iscale[i]), P);
             };
-            const bool pairs = kInt4 && !sides.f32;
+            constexpr bool pairs = kInt4 && !kF32;
             if (pairs) {
             } else if (kInt4) int4_planes(0);
             else build_planes(cpair, absmax_hat(q, sc, mu), P);
@@ -395,7 +408,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    if (kInt4 == 2 && c == 4) int4_planes(1);
+                    if (kGroups == 2 && c == 4) int4_planes(1);
                     if (kInt4 && (c << share) >> 3 != part) continue;
                     const uint32_t x = w[c] ^ 0x88888888u;
                     uint32_t o0, o1, o2, o3;
@@ -768,18 +781,22 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
                         const float* absmax_scale, const float* absmax_offset, int64_t n, int64_t k, void* Y,
                         bool y_bf16, int32_t* dev_status, const LoraArgs& lora, int codebook,
                         uint32_t test_flags, const DeviceInfo& dev, cudaStream_t stream, const Int4Args* w4) {
-    static bool attr_set[64][8] = {};
+    static bool attr_set[64][12] = {};
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     const bool lo = lora.t != nullptr;
-    const int fmt = !w4 ? 0 : (w4->group == 32 ? 2 : 1);
-    const void* fns[8] = {reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 0>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 0>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, true, 0>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, true, 0>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 1>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 1>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 2>),
-                          reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 2>)};
+    const int fmt = !w4 ? 0 : (w4->group == 32 ? 2 : 1) + (w4->scale_f32 ? 2 : 0);
+    const void* fns[12] = {reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 0>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 0>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, true, 0>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, true, 0>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 1>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 1>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 2>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 2>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 1 + gemm::kInt4F32>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 1 + gemm::kInt4F32>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<false, false, 2 + gemm::kInt4F32>),
+                           reinterpret_cast<const void*>(&gemm::k_nf4_gemm<true, false, 2 + gemm::kInt4F32>)};
     const int vi = (y_bf16 ? 1 : 0) + (fmt ? 2 + 2 * fmt : (lo ? 2 : 0));
     const void* fn = fns[vi];
     few::Weight sides = {};  // scales and zero points
@@ -787,7 +804,6 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         sides.scale = w4->scale;
         sides.zero = w4->zero;
         sides.per = static_cast<int>(w4->group / gemm::kBK);  // stages of a group
-        sides.f32 = w4->scale_f32 ? 1 : 0;
     }
     {
         static std::mutex mu;
@@ -850,7 +866,11 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         case 4: NF4_GEMM_LAUNCH(false, false, 1); break;
         case 5: NF4_GEMM_LAUNCH(true, false, 1); break;
         case 6: NF4_GEMM_LAUNCH(false, false, 2); break;
-        default: NF4_GEMM_LAUNCH(true, false, 2); break;
+        case 7: NF4_GEMM_LAUNCH(true, false, 2); break;
+        case 8: NF4_GEMM_LAUNCH(false, false, 1 + gemm::kInt4F32); break;
+        case 9: NF4_GEMM_LAUNCH(true, false, 1 + gemm::kInt4F32); break;
+        case 10: NF4_GEMM_LAUNCH(false, false, 2 + gemm::kInt4F32); break;
+        default: NF4_GEMM_LAUNCH(true, false, 2 + gemm::kInt4F32); break;
     }
 #undef NF4_GEMM_LAUNCH
     return e;
