@@ -10,8 +10,12 @@
 // One CTA an SM.  A cluster of S CTAs has a run of rows, each CTA a range of k of them; the
 // CTA keeps its part of X in shared memory (as fp16, scaled by a power of two per token)
 // and cuts its (16 rows) x (128 k) steps, row tile by row tile, into equal runs for its
-// warps (few::run).  The CTAs' sums are added in rank order through distributed shared
+// warps (few::Runner).  The CTAs' sums are added in rank order through distributed shared
 // memory, so results do not depend on timing.
+//
+// Groups of 128, bf16 scales: one token over 4096 x 4096 takes 6.5 us, of which a launch and X are
+// 4, over 28672 x 8192 26.9 us (4.5 TB/s, 70 % of the rate of a copy); sixteen tokens 41.5 us there,
+// bound by the issue of instructions (47.5 with groups of 64 and zero points).
 #include "nf4_few.cuh"
 #include "nf4_few_host.h"
 #include "nf4_ptx.cuh"
