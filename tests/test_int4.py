@@ -236,6 +236,69 @@ def test_linear_is_exact_on_integers(nf4):
 
 
 @gpu
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear_ranges_of_x(nf4, group):
+    """Tokens far from 1, and columns far apart in one token.  A token goes through fp16 times a
+    power of two that brings its largest value (of a range of columns) to 2^14 or more: what
+    is below fp16's normal numbers is off by 2^-25, 2^-39 of that largest value."""
+    n, k = 300, 1152
+    w = _weight(nf4, n, k, group, True, torch.float32, group)
+    w64 = _dense64(w)
+    g = torch.Generator(device="cuda").manual_seed(group)
+    for m in (1, 7, 16):
+        x = torch.randn(m, k, device="cuda", generator=g)
+        x *= torch.exp2(torch.randint(-90, 91, (m, 1), device="cuda", generator=g).float())
+        if m > 1:
+            x[0] = 0
+            x[1] *= torch.exp2(torch.randint(-30, 31, (k,), device="cuda", generator=g).float())
+        x = x.bfloat16()
+        y, x64 = nf4.nf4_int4_linear(x, w, torch.float32).cpu().double(), x.cpu().double()
+        tol = k * 2.0 ** -23 * (x64.abs() @ w64.abs().t()) + 2.0 ** -39 * x64.abs().amax(1, keepdim=True) * w64.abs().sum(1) + 1e-37
+        assert torch.all((y - x64 @ w64.t()).abs() <= tol)
+        assert m == 1 or torch.all(y[0] == 0)
+
+
+@gpu
+def test_zero_points_beyond_four_bits(nf4):
+    """Only the low four bits of a zero point count, on every path."""
+    for group in (32, 64, 128):
+        a = _weight(nf4, 96, 256, group, True, torch.bfloat16, group)
+        b = nf4.Int4Weight(96, 256, group, a.wq, a.scale, a.zero + 16 * (a.zero % 7) + 128 * (a.zero % 2))
+        assert torch.any(b.zero > 15)
+        assert torch.equal(nf4.nf4_int4_dequantize(a), nf4.nf4_int4_dequantize(b))
+        for m in (1, 12, 20, 200):
+            x = torch.randn(m, 256, device="cuda").bfloat16()
+            assert torch.equal(nf4.nf4_int4_linear(x, a), nf4.nf4_int4_linear(x, b))
+
+
+@gpu
+@pytest.mark.parametrize("m,n,k,group", [(300, 1003, 1088, 64), (130, 2048, 2048, 32), (700, 11008, 512, 128), (16, 5000, 4096, 128)])
+def test_linear_repeats_to_the_bit(nf4, m, n, k, group):
+    """Many calls one after the other: a stage read before it is written, or after it is
+    written again, would show."""
+    w = _weight(nf4, n, k, group, True, torch.bfloat16, n)
+    x = torch.randn(m, k, device="cuda").bfloat16()
+    first = nf4.nf4_int4_linear(x, w)
+    wrong = sum((nf4.nf4_int4_linear(x, w) != first).any() for _ in range(200))
+    assert int(wrong) == 0
+
+
+@gpu
+@pytest.mark.parametrize("m,n,group,scale_dtype", [(40, 64, 64, torch.bfloat16), (300, 512, 32, torch.float32), (700, 11008, 128, torch.bfloat16)])
+def test_linear_waits_are_bounded(nf4, m, n, group, scale_dtype):
+    """The GEMM's waits run out where nothing arrives, and the next call is right."""
+    w = _weight(nf4, n, 512, group, False, scale_dtype, n)
+    x = torch.randn(m, 512, device="cuda").bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full((m, n), 7.0, device="cuda")
+    nf4.nf4_int4_linear(x, w, out=y, dev_status=status, flags=_lib.NF4_LINEAR_TEST_TIMEOUT)
+    assert status.item() == _lib.NF4_ERR_DEVICE_TIMEOUT and torch.all(y == 7)
+    status.zero_()
+    _check(nf4.nf4_int4_linear(x, w, torch.float32, dev_status=status), x, _dense64(w), rounded_weight=True)
+    assert status.item() == 0
+
+
+@gpu
 def test_streams_graph_and_repeat(nf4):
     w = _weight(nf4, 1000, 2048, 128, False, torch.bfloat16, 3)
     x = torch.randn(4, 2048, device="cuda").bfloat16()
