@@ -153,9 +153,12 @@ class NF4Weight:
     absmax_offset: torch.Tensor
     quant_type: str = "nf4"
 
-    def struct(self) -> nf4_weight_t:
+    def _struct_ref(self):
         return _kept_struct(self, (self.n, self.k, self.quant_type, self.wq.data_ptr(), self.absmax_q.data_ptr(),
-                                   self.absmax_scale.data_ptr(), self.absmax_offset.data_ptr()))[1]
+                                   self.absmax_scale.data_ptr(), self.absmax_offset.data_ptr()))
+
+    def struct(self) -> nf4_weight_t:
+        return self._struct_ref()[1]
 
     def _make(self, key):
         magic = _lib.NF4_FP4_WEIGHT_MAGIC if self.quant_type == "fp4" else _lib.NF4_WEIGHT_MAGIC
@@ -475,13 +478,13 @@ def nf4_int4_quantize(W: torch.Tensor, group: int = 128, symmetric: bool = True,
     else:
         _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
     if scale is None:
-        scale = torch.empty((k // group, n), dtype=scale_dtype, device=dev)
+        scale = torch.empty(k // group, n, dtype=scale_dtype, device=dev)
     else:
         _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
     if zero is not None:
         _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
     elif not symmetric:
-        zero = torch.empty((k // group, n), dtype=torch.uint8, device=dev)
+        zero = torch.empty(k // group, n, dtype=torch.uint8, device=dev)
     _launch(dev.index, stream, _lib.lib().nf4_int4_quantize, "nf4_int4_quantize", W.data_ptr(), _DTYPES[W.dtype], n, k, group,
             _DTYPES[scale_dtype], wq.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
     return wq, scale, zero
@@ -501,7 +504,7 @@ def nf4_int4_dequantize(weight: Int4Weight, dtype=torch.bfloat16, out: torch.Ten
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError("dtype must be float32 or bfloat16")
-        out = torch.empty((weight.n, weight.k), dtype=dtype, device=dev)
+        out = torch.empty(weight.n, weight.k, dtype=dtype, device=dev)
     else:
         _check_out(out, (weight.n, weight.k), _DTYPES, dev, "out")
     _launch(dev.index, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._struct_ref()[2], out.data_ptr(),
@@ -525,7 +528,7 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError("dtype must be float32 or bfloat16")
-        out = torch.empty((m, weight.n), dtype=dtype, device=dev)
+        out = torch.empty(m, weight.n, dtype=dtype, device=dev)
     else:
         _check_out(out, (m, weight.n), _DTYPES, dev, "out")
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
@@ -578,13 +581,13 @@ def nf4_moe(X: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, re
         raise ValueError("workspace must be a contiguous tensor on the device of X")
     ids = probs = None
     if return_routing:
-        ids = torch.empty((m, top_k), dtype=torch.int32, device=X.device)
-        probs = torch.empty((m, top_k), dtype=torch.float32, device=X.device)
+        ids = torch.empty(m, top_k, dtype=torch.int32, device=X.device)
+        probs = torch.empty(m, top_k, dtype=torch.float32, device=X.device)
     L = _lib.lib()
     if integer:
         fn, where, gu, dn = L.nf4_int4_moe, "nf4_int4_moe", gate_up._struct_ref()[2], down._struct_ref()[2]
     else:
-        fn, where, gu, dn = L.nf4_moe, "nf4_moe", ctypes.byref(gate_up.struct()), ctypes.byref(down.struct())
+        fn, where, gu, dn = L.nf4_moe, "nf4_moe", gate_up._struct_ref()[2], down._struct_ref()[2]
     _launch(index, stream, fn, where, X.data_ptr(), m, router.data_ptr(), n_experts, gu, dn, top_k, out.data_ptr(),
             None if ids is None else ids.data_ptr(), None if probs is None else probs.data_ptr(),
             _lib.NF4_MOE_RENORMALIZE if renormalize else 0, workspace.data_ptr(),
