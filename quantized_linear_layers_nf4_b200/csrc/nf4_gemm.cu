@@ -30,10 +30,11 @@
 //   store Y.
 // Integer codes (kInt4) take the same way with three differences.  Two teams of eight decoding
 // warps take the stages in turn, since a warp spends most of a stage waiting; a tile has 32 to 256
-// weight rows, as the number of tiles asks (tile_rows), and its rows are shared by the threads of a
-// team; and up to 128 tokens only half of the token tile is multiplied.  512 tokens over
-// 11008 x 4096 take 45 us (1026 TFLOP/s; with one team and 256 rows 60), 128 over 4096 x 4096
-// 25 us.  A stage takes 750 to 1300 cycles, of which the MMAs are 128 to 1024: bound by what a
+// weight rows and k is split over a cluster of up to 8 CTAs, as the number of tiles asks
+// (plan_int4), the threads of a team share a small tile's rows, and the CTAs' sums are added in rank
+// order through distributed shared memory; and up to 128 tokens only half of the token tile is
+// multiplied.  512 tokens over 11008 x 4096 take 45 us (1026 TFLOP/s; with one team and 256 rows 60),
+// 128 over 4096 x 4096 14 us.  A stage takes 750 to 1300 cycles, of which the MMAs are 128 to 1024: bound by what a
 // decoding warp has to issue and wait for.
 // Every mbarrier wait is bounded; a wait that runs out records
 // NF4_ERR_DEVICE_TIMEOUT, the CTA drains what it issued and frees its tensor
@@ -42,7 +43,7 @@
 
 #include "nf4_common.cuh"
 #include "nf4_decode.cuh"
-#include "nf4_few.cuh"
+#include "nf4_few_host.h"
 #include "nf4_internal.h"
 #include "nf4_ptx.cuh"
 #include "nf4_tmap.h"
@@ -62,6 +63,7 @@ constexpr int kPBytes = kBN * kBK / 2;  // 8192
 constexpr int kDequantWarps = 8;
 constexpr int kThreads = 32 * (4 + kDequantWarps);
 constexpr int kInt4F32 = 4;
+constexpr int kPartPad = 4;  // words between the rows of a CTA's sums in shared memory, for the banks
 // A decoding warp spends more of a stage waiting than working: two teams of them take turns for integer
 // codes, whose decoding needs few enough registers.
 constexpr int threads_of(int integer) { return integer ? kThreads + 32 * kDequantWarps : kThreads; }
@@ -115,7 +117,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
            const __nv_bfloat16* __restrict__ lora_up, int lora_r, int lora_tc,
            const __grid_constant__ CUtensorMap tm_thi, const __grid_constant__ CUtensorMap tm_tlo,
            const __grid_constant__ CUtensorMap tm_up, int codebook, uint32_t lim, int stall,
-           const few::Weight sides, int tile_n, int x_rows) {
+           const few::Weight sides, int tile_n, int x_rows, int splits) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -137,7 +139,10 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * bn;
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kBM;
     const int halves = kInt4 && m - m0 <= 128 ? 1 : 2;  // of the token tile that hold any
-    const int nk = static_cast<int>(k / kBK);
+    // k over the CTAs of a cluster: this one has stages k0 .. k0 + nk
+    const few::Shares parts = few::shares_of(static_cast<int>(k / kBK), kInt4 ? splits : 1);
+    const int rank = kInt4 ? static_cast<int>(blockIdx.z) : 0, k0 = parts.start(rank);
+    const int nk = parts.start(rank + 1) - k0;
     const uint32_t sbase = smem_u32(smem);
 
     if (threadIdx.x == 0) {
@@ -158,6 +163,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         mbar_init(lora_full, 1);
         mbar_init(mma_done, 1);
         fence_mbar_init();
+        tmem_slot[1] = 0;  // this CTA's part is not valid
     }
     if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
     tc_fence_before();
@@ -182,7 +188,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                     break;
                 }
                 mbar_arrive_expect_tx(&full_a[s], kInt4 ? x_rows * kBK * 2 : kABytes);
-                tma_load_2d(smem + s * kABytes, &tm_x, kt * kBK, static_cast<int32_t>(m0), &full_a[s]);
+                tma_load_2d(smem + s * kABytes, &tm_x, (k0 + kt) * kBK, static_cast<int32_t>(m0), &full_a[s]);
                 issued = kt + 1;
             }
             if (timed_out)  // leave no copy in flight
@@ -201,7 +207,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                     break;
                 }
                 mbar_arrive_expect_tx(&full_p[s], bn * kBK / 2);
-                tma_load_2d(smem + kOffP + s * kPBytes, &tm_w, kt * (kBK / 2), static_cast<int32_t>(n0),
+                tma_load_2d(smem + kOffP + s * kPBytes, &tm_w, (k0 + kt) * (kBK / 2), static_cast<int32_t>(n0),
                             &full_p[s]);
                 issued = kt + 1;
             }
@@ -336,7 +342,11 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             }
         };
         if (kInt4) {
-            if (team) later(team);
+            const int first = k0 + team;
+            const int before = kGroups == 2 ? 2 * first : first / sides.per;
+            gleft -= first - before * sides.per;
+            s_at += before * kScale * n;
+            z_at += before * z_row;
             if (team < nk) fetch_sides();
         }
         for (int kt = team; kt < nk; kt += kTeams) {
@@ -444,6 +454,13 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             uint32_t r[32];
             if (ok) tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 256 + cc * 32, r);
             const int64_t col0 = n0 + cc * 32;
+            if (kInt4 && splits > 1) {  // to shared memory: the rings are done with
+                float* to = reinterpret_cast<float*>(smem) + (half * 128 + quarter * 32 + lane) * (bn + kPartPad) + cc * 32;
+                if (ok && half < halves)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                continue;
+            }
             if (!ok || tok >= m || col0 >= n) continue;
             if (kLora && !lora_tc) {
                 // low-rank term on the CUDA cores (rank not a multiple of 8):
@@ -505,11 +522,58 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             }
         }
     }
-    if (timed_out) record_timeout(dev_status);
+    if (timed_out) {
+        record_timeout(dev_status);
+        tmem_slot[1] = 1;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (!kInt4 || splits == 1) return;
+    // The CTAs' parts are added in rank order, each CTA for its share of the tokens.
+    __syncwarp();
+    cluster_sync();
+    uint32_t failed = 0;
+    for (int s = 0; s < splits; ++s) failed |= ld_shared_cluster_u32(map_shared_rank(smem_u32(tmem_slot + 1), static_cast<uint32_t>(s)));
+    const int toks = x_rows / splits, quads = bn / 4;
+    for (int i = threadIdx.x; i < toks * quads && !failed; i += blockDim.x) {
+        const int row = rank * toks + i / quads, c = i % quads * 4;
+        const int64_t tok = m0 + row, col = n0 + c;
+        if (tok >= m || col >= n) continue;
+        const uint32_t at = sbase + (row * (bn + kPartPad) + c) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s = 0; s < splits; ++s) {
+            const float4 u = ld_shared_cluster_f32x4(map_shared_rank(at, static_cast<uint32_t>(s)));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        if (kBf16Out) {
+            __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(Y) + tok * n + col;
+            if (n % 4 == 0) {
+                *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            } else {
+                const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < n) y[e] = __float2bfloat16_rn(u[e]);
+            }
+        } else {
+            float* y = reinterpret_cast<float*>(Y) + tok * n + col;
+            if (n % 4 == 0) {
+                *reinterpret_cast<float4*>(y) = v;
+            } else {
+                const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < n) y[e] = u[e];
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another still reads its part
 }
 
 // ---------------------------------------------------------------------------
@@ -764,22 +828,32 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Weight rows of a tile for integer codes: a stage takes a time that goes about as 350 + rows,
-// since most of it is the decoding warps' latency, and the waves of tiles over the SMs go in
-// whole numbers.  512 x 11008x4096 takes 48 us with 160 rows (69 x 2 tiles) and 59 with 256
-// (43 x 2); 256 x 4096x4096 32 us with 32 rows and 53 with 256.  `cost`: of all stages of one k.
-int tile_rows(int64_t m, int64_t n, int sms, int64_t* cost) {
-    int best = kBN;
-    *cost = INT64_MAX;
-    for (int rows = kBN; rows >= 32; rows -= 32) {
-        const int64_t tiles = (n + rows - 1) / rows * ((m + kBM - 1) / kBM);
-        const int64_t c = (tiles + sms - 1) / sms * (350 + rows);
-        if (c < *cost) {
-            *cost = c;
-            best = rows;
+// Tiles for integer codes.  A stage takes a time that goes about as 350 + its weight rows, since
+// most of it is the decoding warps' latency, so that a few large tiles with k split over a cluster
+// beat many small ones, and the waves of tiles over the SMs go in whole numbers.  128 tokens over
+// 4096 x 4096 take 14 us with 256 rows and k in eight parts, 25 with 32 rows and k whole, 44 with 256
+// and whole; 512 over 11008 x 4096, whose tiles leave no SMs for parts, 45 with 160 rows and 59 with 256.
+struct Plan {
+    int rows, splits;
+    double us;
+};
+cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev, Plan* out) {
+    const int64_t token_tiles = (m + kBM - 1) / kBM, stages = k / kBK, x_rows = m <= 128 ? 128 : kBM;
+    const double stage = 0.95e-3 * (m <= 128 ? 1.0 : 1.15);
+    *out = Plan{kBN, 1, 1e30};
+    for (int splits = 1; splits == 1 || (splits <= 8 && stages >= 4 * splits); splits *= 2) {
+        int fit = 0;  // clusters at a time
+        const cudaError_t e = few::resident(reinterpret_cast<const void*>(&k_nf4_gemm<true, false, 1>), threads_of(1), splits, dev, &fit);
+        if (e != cudaSuccess) return e;
+        for (int rows = kBN; rows >= 32; rows -= 32) {
+            if (splits > 1 && x_rows * (rows + kPartPad) * 4 > kOffBar) continue;
+            const int64_t waves = ((n + rows - 1) / rows * token_tiles + fit - 1) / fit;
+            double us = 5.0 + stage * static_cast<double>(waves * ((stages + splits - 1) / splits) * (350 + rows));
+            if (splits > 1) us += 1.5 + 3e-5 * static_cast<double>(x_rows * rows * waves);
+            if (us < out->us) *out = Plan{rows, splits, us};
         }
     }
-    return best;
+    return cudaSuccess;
 }
 
 }  // namespace gemm
@@ -823,8 +897,12 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
         }
     }
     const int x_rows = w4 && m <= 128 ? 128 : gemm::kBM;
-    int64_t cost = 0;
-    const int bn = w4 ? gemm::tile_rows(m, n, dev.sm_count, &cost) : gemm::kBN;
+    gemm::Plan plan = {gemm::kBN, 1, 0.0};
+    if (w4) {
+        const cudaError_t pe = gemm::plan_int4(m, n, k, dev, &plan);
+        if (pe != cudaSuccess) return pe;
+    }
+    const int bn = plan.rows;
     CUtensorMap tm_x, tm_w;
     cudaError_t e = tmap_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, static_cast<uint64_t>(k),
                             static_cast<uint64_t>(m), static_cast<uint64_t>(k * 2), gemm::kBK, x_rows,
@@ -833,8 +911,8 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
     e = tmap_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, static_cast<uint64_t>(k / 2), static_cast<uint64_t>(n),
                 static_cast<uint64_t>(k / 2), gemm::kBK / 2, bn, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((n + bn - 1) / bn),
-                    static_cast<unsigned>((m + gemm::kBM - 1) / gemm::kBM));
+    const dim3 grid(static_cast<unsigned>((n + bn - 1) / bn), static_cast<unsigned>((m + gemm::kBM - 1) / gemm::kBM),
+                    static_cast<unsigned>(plan.splits));
     // the low-rank term on the tensor cores needs 16-byte rows of t_hi / t_lo / up (r % 8 == 0)
     int lora_tc = 0;
     CUtensorMap tm_thi = tm_x, tm_tlo = tm_x, tm_up = tm_x;  // unused unless lora_tc
@@ -854,17 +932,20 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = static_cast<unsigned>(plan.splits);
     cfg.attrs = attr;
-    cfg.numAttrs = w4 ? 1 : 0;
+    cfg.numAttrs = !w4 ? 0 : (plan.splits > 1 ? 2 : 1);
 #define NF4_GEMM_LAUNCH(B, L, F)                                                                               \
     cfg.blockDim = dim3(gemm::threads_of(F));                                                                  \
     cfg.dynamicSmemBytes = gemm::kSmemBytes;                                                                   \
     e = cudaLaunchKernelEx(&cfg, gemm::k_nf4_gemm<B, L, F>, tm_x, tm_w, absmax_q, absmax_scale, absmax_offset, m, n, k, Y, \
                            dev_status, lora.t, lora.up, lora.r, lora_tc, tm_thi, tm_tlo, tm_up, codebook,       \
-                           (test_flags & kTestStall) ? 64u : kWaitLimit, (test_flags & kTestStall) ? 1 : 0, sides, bn, x_rows)
+                           (test_flags & kTestStall) ? 64u : kWaitLimit, (test_flags & kTestStall) ? 1 : 0, sides, bn, x_rows, plan.splits)
     switch (vi) {
         case 0: NF4_GEMM_LAUNCH(false, false, 0); break;
         case 1: NF4_GEMM_LAUNCH(true, false, 0); break;
@@ -884,9 +965,8 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
 }
 
 double int4_gemm_us(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev) {
-    int64_t cost = 0;
-    gemm::tile_rows(m, n, dev.sm_count, &cost);
-    return 5.0 + 0.95e-3 * static_cast<double>(cost) * static_cast<double>(k / gemm::kBK);
+    gemm::Plan plan = {};
+    return gemm::plan_int4(m, n, k, dev, &plan) == cudaSuccess ? plan.us : 1e30;
 }
 
 cudaError_t launch_gemm_dx(const void* dY, int64_t m, const uint8_t* wq, const int8_t* absmax_q,

@@ -200,8 +200,8 @@ static int64_t tokens_of_pass(int64_t m, const Int4Args& w) {
 }
 
 // A pass takes 6.7 us over 1024 x 4096, 8.0 over 4096 x 4096, 12 over 11008 x 4096, 41 over
-// 28672 x 8192 and 14 over 512 x 65536: 6 us, 3.2 TB/s and X.  The GEMM (int4_gemm_us) takes 27 us
-// over 4096 x 4096, 32 over 11008 x 4096 and 78 over 28672 x 8192 for any number of tokens up to 128.
+// 28672 x 8192 and 14 over 512 x 65536: 6 us, 3.2 TB/s and X.  The GEMM (int4_gemm_us) takes 14 us
+// over 4096 x 4096, 24 over 11008 x 4096 and 77 over 28672 x 8192 for any number of tokens up to 128.
 bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev) {
     if (m <= kGemvMaxTokens) return true;
     const double k = static_cast<double>(w.k), pass = 6.0 + static_cast<double>(w.n) * k * 0.5 / 3.2e6 + k * 5e-5;

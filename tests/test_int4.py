@@ -272,7 +272,7 @@ def test_zero_points_beyond_four_bits(nf4):
 
 
 @gpu
-@pytest.mark.parametrize("m,n,k,group", [(300, 1003, 1088, 64), (130, 2048, 2048, 32), (700, 11008, 512, 128), (16, 5000, 4096, 128)])
+@pytest.mark.parametrize("m,n,k,group", [(300, 1003, 1088, 64), (130, 2048, 2048, 32), (700, 11008, 512, 128), (16, 5000, 4096, 128), (77, 130, 8192, 64)])
 def test_linear_repeats_to_the_bit(nf4, m, n, k, group):
     """Many calls one after the other: a stage read before it is written, or after it is
     written again, would show."""
@@ -284,7 +284,7 @@ def test_linear_repeats_to_the_bit(nf4, m, n, k, group):
 
 
 @gpu
-@pytest.mark.parametrize("m,n,group,scale_dtype", [(40, 64, 64, torch.bfloat16), (300, 512, 32, torch.float32), (700, 11008, 128, torch.bfloat16)])
+@pytest.mark.parametrize("m,n,group,scale_dtype", [(40, 64, 64, torch.bfloat16), (300, 512, 32, torch.float32), (700, 11008, 128, torch.bfloat16), (600, 4096, 128, torch.bfloat16)])
 def test_linear_waits_are_bounded(nf4, m, n, group, scale_dtype):
     """The GEMM's waits run out where nothing arrives, and the next call is right."""
     w = _weight(nf4, n, 512, group, False, scale_dtype, n)
@@ -345,10 +345,11 @@ def test_weights_are_copied_and_saved(nf4, kind):
 @gpu
 def test_linear_from_few_to_many_tokens(nf4):
     """Around every change of path the result is within that of a weight rounded to bf16."""
-    for n, k in ((64, 4096), (4096, 1024), (40000, 128)):
-        w = _weight(nf4, n, k, 128, True, torch.bfloat16, n)
+    for n, k, group, zero, dtype in ((64, 4096, 128, True, torch.bfloat16), (4096, 1024, 128, False, torch.float32), (40000, 128, 128, True, torch.bfloat16),
+                                     (333, 5184, 32, True, torch.float32), (1001, 8128, 64, False, torch.bfloat16), (96, 13440, 192, True, torch.float32)):
+        w = _weight(nf4, n, k, group, zero, dtype, n)
         w64 = _dense64(w)
-        for m in (16, 17, 31, 32, 33, 48, 64, 65, 96, 127, 128, 129):
+        for m in (16, 17, 31, 32, 33, 48, 64, 65, 96, 127, 128, 129, 256, 257):
             x = torch.randn(m, k, device="cuda").bfloat16()
             _check(nf4.nf4_int4_linear(x, w, torch.float32), x, w64, rounded_weight=True)
 
