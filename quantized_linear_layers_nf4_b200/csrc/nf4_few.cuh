@@ -26,7 +26,7 @@
 //   kTable codebook levels with the absmax of each 64: as kG64
 // The copies and what feeds them reach 5.4 TB/s without the products; what the products add is the
 // issue of about 9 instructions a word of codes (integer), or a look-up a byte in a table in shared
-// memory (codebook: L1's data pipe is 84 % busy then).
+// memory (codebook: L1's data pipe is 70 % busy over a whole kernel, 84 % at its best).
 // Scales go to registers, four groups of a row at a time (a window: kG128 four steps, kG64 and
 // kTable two, kG32 one): lane (g, t) loads that of group t for its rows, one window ahead, and a
 // shuffle hands it to the other lanes of the row.
