@@ -464,9 +464,10 @@ __device__ __forceinline__ Shares shares_of_warps(int total) {
 //   ahead(step)          before the step's codes are waited for
 //   mul(entry, step)     multiplies a step of the tile, counted from the row's first
 //   finish(tile)         its sums are complete in acc
-// kFour: the inner loop takes four steps at a time where it can; without it the code and its
-// registers stay small enough for the mixture-of-experts kernels.
-template <int F, bool Z, int kDepth, int NT, bool kFour>
+// One step at a time: four in a row, with constant windows and offsets, took 1.6 % less over 28672 x 8192
+// but 3 to 11 % more over 4096 x 4096 and 1024 x 4096, whose time is in fetching the code, and
+// with the experts' registers more throughout.
+template <int F, bool Z, int kDepth, int NT>
 struct Runner {
     static constexpr int kR = window_steps<F>();
     Sides<F, Z> side;
@@ -495,24 +496,19 @@ struct Runner {
         }
     }
     template <typename Rows>
-    __device__ __forceinline__ void moved(const Weight& w, int n, Rows&& rows) {  // n steps were sent
-        sent += n;
-        step += n;
-        if (step == s0 + ns) {
-            step = s0;
-            ++tile;
-            if (sent < i1) {
-                int64_t row[2];
-                rows(tile, row);
-                aim_codes(w, row);
-            }
-        }
-    }
-    template <typename Rows>
     __device__ __forceinline__ void send(const Weight& w, uint32_t entry, Rows&& rows) {
         if (sent < i1) {
             copy(w, entry, static_cast<uint32_t>(step) * (kStepK / 2u));
-            moved(w, 1, rows);
+            ++sent;
+            if (++step == s0 + ns) {
+                step = s0;
+                ++tile;
+                if (sent < i1) {
+                    int64_t row[2];
+                    rows(tile, row);
+                    aim_codes(w, row);
+                }
+            }
         }
         copies_commit();
     }
@@ -582,44 +578,16 @@ struct Runner {
                 side.turn(w, mu);
                 next_window(w, rows);
             };
-            auto wrap = [&] { entry = entry == (kDepth - 1) * kStepBytes ? 0u : entry + kStepBytes; };
-            auto ready = [&](int step) {
-                ahead(step);
-                copies_wait<kDepth - 1>();
-                if (F != kG128) __syncwarp();  // else a lane reads what it copied itself
-            };
             turn();
             for (const int end = st + n;;) {
-                if (kFour && (st & 3) == 0 && st + 4 <= end) {
-                    // four steps from a multiple of four on: windows and offsets are constants, and
-                    // as a rule the four that follow are one more piece of the same rows
-                    const unsigned q = static_cast<unsigned>(st) >> 2;
-                    const bool plain = sent + 4 <= i1 && step + 4 <= s0 + ns;
-                    const uint32_t to = static_cast<uint32_t>(step) * (kStepK / 2u);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        if (s > 0 && s % kR == 0) turn();
-                        ready(static_cast<int>(4 * q + s));
-                        mul(ring + entry, static_cast<int>(4 * q + s));
-                        if (F != kG128) __syncwarp();
-                        if (plain) {
-                            copy(w, entry, to + s * (kStepK / 2u));
-                            copies_commit();
-                        } else {
-                            send(w, entry, rows);
-                        }
-                        wrap();
-                    }
-                    if (plain) moved(w, 4, rows);
-                    st += 4;
-                } else {
-                    ready(st);
-                    mul(ring + entry, st);
-                    if (F != kG128) __syncwarp();
-                    send(w, entry, rows);
-                    wrap();
-                    ++st;
-                }
+                ahead(st);
+                copies_wait<kDepth - 1>();
+                if (F != kG128) __syncwarp();  // else a lane reads what it copied itself
+                mul(ring + entry, st);
+                if (F != kG128) __syncwarp();
+                send(w, entry, rows);
+                entry = entry == (kDepth - 1) * kStepBytes ? 0u : entry + kStepBytes;
+                ++st;
                 if (st == end) break;
                 if (st % kR == 0) turn();
             }

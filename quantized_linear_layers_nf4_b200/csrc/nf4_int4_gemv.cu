@@ -13,9 +13,9 @@
 // warps (few::Runner).  The CTAs' sums are added in rank order through distributed shared
 // memory, so results do not depend on timing.
 //
-// Groups of 128, bf16 scales: one token over 4096 x 4096 takes 6.5 us, of which a launch and X are
-// 4, over 28672 x 8192 26.9 us (4.5 TB/s, 70 % of the rate of a copy); sixteen tokens 41.5 us there,
-// bound by the issue of instructions (47.5 with groups of 64 and zero points).
+// Groups of 128, bf16 scales: one token over 4096 x 4096 takes 6.2 us, of which a launch and X are
+// 4, over 28672 x 8192 27.4 us (4.4 TB/s, 69 % of the rate of a copy); sixteen tokens 42.4 us there,
+// bound by the issue of instructions (48.3 with groups of 64 and zero points).
 #include "nf4_few.cuh"
 #include "nf4_few_host.h"
 #include "nf4_ptx.cuh"
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_int4_gemv(const __grid_const
         row[0] = min(static_cast<int64_t>(grp) * 8 + g, a.w.n - 1);
         row[1] = grp + 1 < g1 ? min(static_cast<int64_t>(grp) * 8 + 8 + g, a.w.n - 1) : row[0];
     };
-    few::Runner<F, Z, depth_of(NT), NT, true> R;
+    few::Runner<F, Z, depth_of(NT), NT> R;
     R.find(a.w, smem + a.ring_at, warp, lane, runs, s0, ns, rows_of);
     if (!a.early) grid_dependency_wait();
     R.start(a.w, rows_of);
@@ -199,7 +199,7 @@ static int64_t tokens_of_pass(int64_t m, const Int4Args& w) {
     return most;
 }
 
-// A pass takes 6.7 us over 1024 x 4096, 8.0 over 4096 x 4096, 12 over 11008 x 4096, 41 over
+// A pass takes 7 us over 1024 x 4096, 9 over 4096 x 4096, 14 over 11008 x 4096, 42 over
 // 28672 x 8192 and 14 over 512 x 65536: 6 us, 3.2 TB/s and X.  The GEMM (int4_gemm_us) takes 14 us
 // over 4096 x 4096, 24 over 11008 x 4096 and 77 over 28672 x 8192 for any number of tokens up to 128.
 bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev) {

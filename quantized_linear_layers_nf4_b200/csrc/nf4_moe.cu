@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_gate_up(const __grid_con
         row[0] = static_cast<int64_t>(R.list[idx]) * 2 * p.f + (t0 + tile - idx * per_e) * 8 + g;
         row[1] = row[0] + p.f;
     };
-    few::Runner<F, Z, kDepth, 1, false> run;
+    few::Runner<F, Z, kDepth, 1> run;
     run.find(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
     run.start(w, rows_of);
 
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_down(const __grid_consta
         // where the second half is another CTA's, the first takes its place and is not stored
         row[1] = row[0] + (grp + 1 < g1 ? 8 : 0);
     };
-    few::Runner<F, Z, kDepth, 1, false> run;
+    few::Runner<F, Z, kDepth, 1> run;
     run.find(w, smem + p.ring_at, warp, lane, runs, 0, ns, rows_of);
     run.start(w, rows_of);
     grid_dependency_wait();
