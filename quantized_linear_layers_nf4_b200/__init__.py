@@ -30,9 +30,15 @@ calls.  Functions carry the C names:
 ``quantize_weight(W)`` runs the first two and returns an ``NF4Weight``.  Every
 quantizing call takes ``quant_type="nf4"`` (the default) or ``"fp4"``; an
 ``NF4Weight`` remembers which codebook its codes index.
+
+With ``stream=`` a call runs on that stream, and the tensors it makes belong to it, as
+under ``torch.cuda.stream(stream)``.  The usual rules follow: its inputs must be ready
+there, and a tensor of one stream that another still uses when its last reference goes
+needs ``Tensor.record_stream``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -68,6 +74,16 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _memory_of(stream):
+    """What is allocated inside belongs to the stream that the call runs on.  A block of the
+    current stream's would be one that work queued there may still use, and dropped it could go
+    to a third stream while this one writes it."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
 def _ptr(t: torch.Tensor) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
@@ -95,10 +111,11 @@ def nf4_quantize(W: torch.Tensor, wq: torch.Tensor | None = None, absmax: torch.
         raise ValueError("W must be a 2-D float32 or bfloat16 tensor")
     n, k = W.shape
     numel = n * k
-    if wq is None:
-        wq = torch.empty(numel // 2, dtype=torch.uint8, device=W.device)
-    if absmax is None:
-        absmax = torch.empty(numel // 64, dtype=torch.float32, device=W.device)
+    with _memory_of(stream):
+        if wq is None:
+            wq = torch.empty(numel // 2, dtype=torch.uint8, device=W.device)
+        if absmax is None:
+            absmax = torch.empty(numel // 64, dtype=torch.float32, device=W.device)
     _lib.check(_lib.lib().nf4_quantize_typed(_ptr(W), _DTYPES[W.dtype], n, k, qt, _ptr(wq), _ptr(absmax),
                                              _stream(stream)), "nf4_quantize")
     return wq, absmax
@@ -113,14 +130,15 @@ def nf4_double_quant(absmax: torch.Tensor, absmax_q: torch.Tensor | None = None,
     nb = absmax.numel()
     L = _lib.lib()
     ws_bytes = L.nf4_double_quant_workspace_bytes(nb)
-    if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 8) // 8 + 1, dtype=torch.float64, device=absmax.device)
-    if absmax_q is None:
-        absmax_q = torch.empty(nb, dtype=torch.int8, device=absmax.device)
-    if absmax_scale is None:
-        absmax_scale = torch.empty((nb + 255) // 256, dtype=torch.float32, device=absmax.device)
-    if absmax_offset is None:
-        absmax_offset = torch.empty(1, dtype=torch.float32, device=absmax.device)
+    with _memory_of(stream):
+        if workspace is None:
+            workspace = torch.empty(max(ws_bytes, 8) // 8 + 1, dtype=torch.float64, device=absmax.device)
+        if absmax_q is None:
+            absmax_q = torch.empty(nb, dtype=torch.int8, device=absmax.device)
+        if absmax_scale is None:
+            absmax_scale = torch.empty((nb + 255) // 256, dtype=torch.float32, device=absmax.device)
+        if absmax_offset is None:
+            absmax_offset = torch.empty(1, dtype=torch.float32, device=absmax.device)
     _lib.check(L.nf4_double_quant(_ptr(absmax), nb, _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _ptr(absmax_q),
                                   _ptr(absmax_scale), _ptr(absmax_offset), _stream(stream)),
@@ -182,7 +200,8 @@ def nf4_dequantize(weight: NF4Weight, dtype=torch.bfloat16, out: torch.Tensor | 
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
     if out is None:
-        out = torch.empty((weight.n, weight.k), dtype=dtype, device=weight.wq.device)
+        with _memory_of(stream):
+            out = torch.empty((weight.n, weight.k), dtype=dtype, device=weight.wq.device)
     st = weight.struct()
     _lib.check(_lib.lib().nf4_dequantize(ctypes.byref(st), _ptr(out), _DTYPES[dtype],
                                          _stream(stream)), "nf4_dequantize")
@@ -197,7 +216,8 @@ def nf4_dequantize_batch(weights, dtype=torch.bfloat16, outs=None, stream=None):
     weights = list(weights)
     count = len(weights)
     if outs is None:
-        outs = [torch.empty((w.n, w.k), dtype=dtype, device=w.wq.device) for w in weights]
+        with _memory_of(stream):
+            outs = [torch.empty((w.n, w.k), dtype=dtype, device=w.wq.device) for w in weights]
     for o in outs:
         _need_cuda(o, "out")
     structs = [w.struct() for w in weights]
@@ -248,7 +268,8 @@ def nf4_linear(X: torch.Tensor, weight: NF4Weight, dtype=torch.bfloat16,
         raise ValueError("dtype must be float32 or bfloat16")
     m = X.shape[0]
     if out is None:
-        out = torch.empty((m, weight.n), dtype=dtype, device=X.device)
+        with _memory_of(stream):
+            out = torch.empty((m, weight.n), dtype=dtype, device=X.device)
     st = weight.struct()
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
@@ -292,7 +313,8 @@ def nf4_linear_group(X: torch.Tensor, weights, dtype=torch.bfloat16, outs=None,
     count = len(weights)
     m = X.shape[0]
     if outs is None:
-        outs = [torch.empty((m, w.n), dtype=dtype, device=X.device) for w in weights]
+        with _memory_of(stream):
+            outs = [torch.empty((m, w.n), dtype=dtype, device=X.device) for w in weights]
     structs = [w.struct() for w in weights]
     wptrs = (ctypes.POINTER(nf4_weight_t) * max(count, 1))(*[ctypes.pointer(s) for s in structs])
     yptrs = (ctypes.c_void_p * max(count, 1))(*[o.data_ptr() for o in outs])
@@ -315,7 +337,8 @@ def nf4_linear_dx(dY: torch.Tensor, weight: NF4Weight, dtype=torch.bfloat16,
         raise ValueError("dtype must be float32 or bfloat16")
     m = dY.shape[0]
     if out is None:
-        out = torch.empty((m, weight.k), dtype=dtype, device=dY.device)
+        with _memory_of(stream):
+            out = torch.empty((m, weight.k), dtype=dtype, device=dY.device)
     st = weight.struct()
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
     _lib.check(_lib.lib().nf4_linear_dx(_ptr(dY), m, ctypes.byref(st), _ptr(out), _DTYPES[dtype], ds,
@@ -348,7 +371,8 @@ def nf4_linear_lora(X: torch.Tensor, weight: NF4Weight, down: torch.Tensor, up: 
         raise ValueError("dtype must be float32 or bfloat16")
     m = X.shape[0]
     if out is None:
-        out = torch.empty((m, weight.n), dtype=dtype, device=X.device)
+        with _memory_of(stream):
+            out = torch.empty((m, weight.n), dtype=dtype, device=X.device)
     st = weight.struct()
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
     flags = _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
@@ -373,11 +397,12 @@ def nf4_merge_lora(weight: NF4Weight, down: torch.Tensor, up: torch.Tensor, scal
         raise ValueError("shapes: down [r, k], up [n, r]")
     numel = weight.n * weight.k
     dev = weight.wq.device
-    if wq is None:
-        wq = torch.empty(numel // 2, dtype=torch.uint8, device=dev)
-    if absmax is None:
-        absmax = torch.empty(numel // 64, dtype=torch.float32, device=dev)
-    w_new = torch.empty((weight.n, weight.k), dtype=torch.bfloat16, device=dev) if want_bf16 else None
+    with _memory_of(stream):
+        if wq is None:
+            wq = torch.empty(numel // 2, dtype=torch.uint8, device=dev)
+        if absmax is None:
+            absmax = torch.empty(numel // 64, dtype=torch.float32, device=dev)
+        w_new = torch.empty((weight.n, weight.k), dtype=torch.bfloat16, device=dev) if want_bf16 else None
     st = weight.struct()
     _lib.check(_lib.lib().nf4_merge_lora(ctypes.byref(st), _ptr(down), _ptr(up), r, float(scale),
                                          ctypes.c_void_p(0) if w_new is None else _ptr(w_new), _ptr(wq),
@@ -473,18 +498,19 @@ def nf4_int4_quantize(W: torch.Tensor, group: int = 128, symmetric: bool = True,
     if not _group_ok(k, group):
         raise ValueError(_GROUP_RULE)
     dev = W.device
-    if wq is None:
-        wq = torch.empty(n * k // 2, dtype=torch.uint8, device=dev)
-    else:
-        _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
-    if scale is None:
-        scale = torch.empty(k // group, n, dtype=scale_dtype, device=dev)
-    else:
-        _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
-    if zero is not None:
-        _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
-    elif not symmetric:
-        zero = torch.empty(k // group, n, dtype=torch.uint8, device=dev)
+    with _memory_of(stream):
+        if wq is None:
+            wq = torch.empty(n * k // 2, dtype=torch.uint8, device=dev)
+        else:
+            _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
+        if scale is None:
+            scale = torch.empty(k // group, n, dtype=scale_dtype, device=dev)
+        else:
+            _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
+        if zero is not None:
+            _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
+        elif not symmetric:
+            zero = torch.empty(k // group, n, dtype=torch.uint8, device=dev)
     _launch(dev.index, stream, _lib.lib().nf4_int4_quantize, "nf4_int4_quantize", W.data_ptr(), _DTYPES[W.dtype], n, k, group,
             _DTYPES[scale_dtype], wq.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
     return wq, scale, zero
@@ -504,7 +530,8 @@ def nf4_int4_dequantize(weight: Int4Weight, dtype=torch.bfloat16, out: torch.Ten
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError("dtype must be float32 or bfloat16")
-        out = torch.empty(weight.n, weight.k, dtype=dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(weight.n, weight.k, dtype=dtype, device=dev)
     else:
         _check_out(out, (weight.n, weight.k), _DTYPES, dev, "out")
     _launch(dev.index, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._struct_ref()[2], out.data_ptr(),
@@ -528,7 +555,8 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError("dtype must be float32 or bfloat16")
-        out = torch.empty(m, weight.n, dtype=dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(m, weight.n, dtype=dtype, device=dev)
     else:
         _check_out(out, (m, weight.n), _DTYPES, dev, "out")
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
@@ -570,19 +598,20 @@ def nf4_moe(X: torch.Tensor, router: torch.Tensor, gate_up, down, top_k: int, re
     if router.get_device() != index or gate_up.wq.get_device() != index or down.wq.get_device() != index:
         raise ValueError("X, router and the weights must be on one device")
     if out is None:
-        out = torch.empty_like(X)
+        with _memory_of(stream):
+            out = torch.empty_like(X)
     else:
         _check_out(out, X.shape, (torch.bfloat16,), X.device, "out")
     if workspace is None:
-        workspace = moe_workspace(h, f, n_experts, top_k, X.device)
-        if stream is not None:
-            workspace.record_stream(stream)  # freed here before that stream is done with it
+        with _memory_of(stream):
+            workspace = moe_workspace(h, f, n_experts, top_k, X.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of X")
     ids = probs = None
     if return_routing:
-        ids = torch.empty(m, top_k, dtype=torch.int32, device=X.device)
-        probs = torch.empty(m, top_k, dtype=torch.float32, device=X.device)
+        with _memory_of(stream):
+            ids = torch.empty(m, top_k, dtype=torch.int32, device=X.device)
+            probs = torch.empty(m, top_k, dtype=torch.float32, device=X.device)
     L = _lib.lib()
     if integer:
         fn, where, gu, dn = L.nf4_int4_moe, "nf4_int4_moe", gate_up._struct_ref()[2], down._struct_ref()[2]
