@@ -498,6 +498,9 @@ typedef struct nf4_int4_weight {
  *               z = clamp(rint(-lo / s), 0, 15);
  *   s is rounded to scale_dtype first;  q = clamp(rint(w / s) + z, 0, 15).
  * Where s is 0 the divisions are by 1 (a group of zeros gets q = z).
+ * Weights should be finite.  A NaN has code 15 and does not count for its group's extremes;
+ * where s is infinite (an infinite weight, or hi - lo past the largest fp32) finite weights have
+ * q = z, infinite ones code 15, and an asymmetric z is 0.
  *   W       device, [n, k] of w_dtype, 16-byte aligned
  *   group, scale_dtype, and the outputs wq, scale, zero as in nf4_int4_weight_t
  * Errors: NF4_ERR_NULL, NF4_ERR_DTYPE, NF4_ERR_SHAPE, NF4_ERR_ALIGN (W, wq: 16

@@ -8,7 +8,8 @@
 //
 // Every step is one fp32 operation rounded to nearest even; s is rounded to its
 // storage type before anything is divided by it, so the codes are the best ones for
-// the scale that is kept.  A group of zeros has s = 0 and q = z.
+// the scale that is kept.  A group of zeros has s = 0 and q = z.  A NaN weight gets code 15
+// and does not count for the extremes.
 //
 // Both are bound by HBM: 2 or 4 bytes of weight and half a byte of code per element.
 // Codes are laid out as the NF4 ones are (row-major, element 2i in the high nibble of
@@ -44,7 +45,8 @@ __device__ __forceinline__ void group_params(float lo, float hi, bool f32, float
 // Markstein's range with its rounded reciprocal.  Clamped before it is rounded (the bound is
 // an integer), and from above alone: rint(lo / s) + z is 0 or more, since rint is odd and z
 // was not cut off (s is within 2^-8 of (hi - lo) / 15), and the symmetric form's quotients
-// stay under 7.5.
+// stay under 7.5.  In that form too the minimum is taken: it makes a NaN quotient the largest code,
+// where its sum's bits would reach into the other weights' nibbles.
 template <bool kZero>
 __device__ __forceinline__ uint32_t encode_fast(const float (&v)[8], float d, float r, float z) {
     const uint64_t rr = f2(r, r), nd = f2(-d, -d), magic = f2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
@@ -52,13 +54,11 @@ __device__ __forceinline__ uint32_t encode_fast(const float (&v)[8], float d, fl
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint64_t x = f2(v[2 * i], v[2 * i + 1]), q0 = mul2(x, rr);
-        uint64_t q = fma2(fma2(q0, nd, x), rr, q0), t;
-        if (kZero) {
-            float a, b;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
-            q = f2(fminf(a, 15.0f - z), fminf(b, 15.0f - z));
-        }
-        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(q), "l"(magic));
+        const uint64_t q = fma2(fma2(q0, nd, x), rr, q0);
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
+        uint64_t t;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(f2(fminf(a, 15.0f - z), fminf(b, 15.0f - z))), "l"(magic));
         w += static_cast<uint32_t>(t) * (16u << (8 * i)) + static_cast<uint32_t>(t >> 32) * (1u << (8 * i));
     }
     return w - (0x4B400000u - static_cast<uint32_t>(z)) * 0x11111111u;
@@ -66,10 +66,10 @@ __device__ __forceinline__ uint32_t encode_fast(const float (&v)[8], float d, fl
 template <bool kZero>
 __device__ __forceinline__ uint32_t encode(const float (&v)[8], float d, float r, float z) {
     if (markstein_ok(d)) return encode_fast<kZero>(v, d, r, z);
-    uint32_t w = 0;  // the same by division
+    uint32_t w = 0;  // the same by division, NaN again the largest code
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        w |= static_cast<uint32_t>(fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(v[j], d)), z), 0.0f), 15.0f)) << (8 * (j >> 1) + ((j & 1) ? 0 : 4));
+        w |= static_cast<uint32_t>(fmaxf(fminf(__fadd_rn(rintf(__fdiv_rn(v[j], d)), z), 15.0f), 0.0f)) << (8 * (j >> 1) + ((j & 1) ? 0 : 4));
     return w;
 }
 

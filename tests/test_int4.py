@@ -189,6 +189,41 @@ def test_quantize_ties_and_borders(nf4):
     assert np.array_equal(_unpack(wq, 1, 128), _quantize(W, 128, True, torch.float32)[0])
 
 
+@gpu
+@pytest.mark.parametrize("group", [32, 64, 128, 256, 192])
+@pytest.mark.parametrize("dtype,symmetric", [(torch.bfloat16, True), (torch.bfloat16, False), (torch.float32, True), (torch.float32, False)])
+@pytest.mark.parametrize("size", [0.02, 1e-25])  # the second's divisors are out of the quotient's fast range
+def test_quantize_not_finite(nf4, group, dtype, symmetric, size):
+    """A NaN weight has code 15 and spoils no other weight of its word or group; where a
+    group's scale is infinite a finite weight has the zero point's code."""
+    n, k = 24, 4 * group
+    g = torch.Generator(device="cuda").manual_seed(group)
+    W = (torch.randn(n, k, device="cuda", generator=g) * size).to(dtype)
+    clean = W.clone()
+    for r in range(8):
+        W[r, group + 8 + r] = float("nan")   # every place of a word
+    W[8, :group] = float("nan")              # nothing but NaN
+    W[9, 3:11] = float("nan")                # parts of two words
+    W[10, 5], W[11, 6] = float("inf"), float("-inf")
+    wq, scale, zero = nf4.nf4_int4_quantize(W, group, symmetric, torch.float32)
+    q, s = _unpack(wq, n, k).reshape(n, 4, group), scale.cpu().numpy().T
+    z = np.full((n, 4), 8) if symmetric else zero.cpu().numpy().T
+    w = W.float().cpu().numpy()
+    assert np.all(q.reshape(n, k)[np.isnan(w) | np.isinf(w)] == 15)
+    for r, finite in ((10, np.arange(group) != 5), (11, np.arange(group) != 6)):
+        assert np.isinf(s[r, 0]) and np.all(q[r, 0][finite] == z[r, 0])
+    # as if the NaN had been zeros
+    w[np.isnan(w)] = 0
+    inf = np.isinf(w)
+    w[inf] = clean.float().cpu().numpy()[inf]
+    wantq, wants, wantz = _quantize(torch.from_numpy(w), group, symmetric, torch.float32)
+    same = np.ones((n, 4), bool)
+    same[10:12, 0] = False
+    assert np.array_equal(s[same], wants.T[same]) and np.array_equal(z[same], wantz.T[same])
+    same = np.repeat(same, group, 1) & ~np.isnan(W.float().cpu().numpy())
+    assert np.array_equal(q.reshape(n, k)[same], wantq[same])
+
+
 # ---------------------------------- linear ----------------------------------
 SHAPES = [(1, 64, 64), (1, 64, 32), (15, 128, 128), (16, 192, 64), (17, 448, 448), (40, 1088, 32), (100, 4096, 128),
           (1003, 1088, 64), (2048, 640, 320), (129, 16384, 256), (8, 65536, 65536), (24, 57344, 32), (9000, 1024, 128), (60001, 128, 64)]
