@@ -146,22 +146,32 @@ def nf4_double_quant(absmax: torch.Tensor, absmax_q: torch.Tensor | None = None,
     return absmax_q, absmax_scale, absmax_offset
 
 
-def _kept_struct(weight, key):
-    """(key, C struct, reference to it) of a weight, built again when the key (sizes and
-    data pointers) is not that of the last time."""
-    kept = weight.__dict__.get("_kept")
-    if kept is None or kept[0] != key:
-        st = weight._make(key)
-        kept = weight.__dict__["_kept"] = (key, st, ctypes.byref(st))
-    return kept
+class _KeptStruct:
+    """The C struct that a weight's calls pass, kept beside its fields (not among them, so it
+    is neither copied nor pickled) and built again when the key -- sizes and data pointers --
+    is not that of the last time."""
+    __slots__ = ("_kept",)
 
+    def _struct_ref(self):
+        """(key, C struct, reference to it); shared by all calls, not to be changed."""
+        key = self._key()
+        kept = getattr(self, "_kept", None)
+        if kept is None or kept[0] != key:
+            st = self._make(key)
+            kept = (key, st, ctypes.byref(st))
+            object.__setattr__(self, "_kept", kept)
+        return kept
 
-def _without_struct(self):  # what is copied and pickled
-    return {name: v for name, v in self.__dict__.items() if name != "_kept"}
+    def struct(self):
+        """A C struct of its own that borrows the weight's tensors."""
+        return self._make(self._key())
+
+    def __getstate__(self):
+        return self.__dict__
 
 
 @dataclass
-class NF4Weight:
+class NF4Weight(_KeptStruct):
     """A quantized [n, k] weight: device tensors plus the C struct that borrows them."""
     n: int
     k: int
@@ -171,18 +181,13 @@ class NF4Weight:
     absmax_offset: torch.Tensor
     quant_type: str = "nf4"
 
-    def _struct_ref(self):
-        return _kept_struct(self, (self.n, self.k, self.quant_type, self.wq.data_ptr(), self.absmax_q.data_ptr(),
-                                   self.absmax_scale.data_ptr(), self.absmax_offset.data_ptr()))
+    def _key(self):
+        return (self.n, self.k, self.quant_type, self.wq.data_ptr(), self.absmax_q.data_ptr(), self.absmax_scale.data_ptr(),
+                self.absmax_offset.data_ptr())
 
-    def struct(self) -> nf4_weight_t:
-        return self._struct_ref()[1]
-
-    def _make(self, key):
+    def _make(self, key) -> nf4_weight_t:
         magic = _lib.NF4_FP4_WEIGHT_MAGIC if self.quant_type == "fp4" else _lib.NF4_WEIGHT_MAGIC
         return nf4_weight_t(magic, _lib.NF4_WEIGHT_VERSION, self.n, self.k, _lib.NF4_BLOCKSIZE, _lib.NF4_BLOCKSIZE2, *key[3:])
-
-    __getstate__ = _without_struct
 
     def nbytes(self) -> int:
         return (self.wq.numel() + self.absmax_q.numel() + 4 * self.absmax_scale.numel())
@@ -202,7 +207,7 @@ def nf4_dequantize(weight: NF4Weight, dtype=torch.bfloat16, out: torch.Tensor | 
     if out is None:
         with _memory_of(stream):
             out = torch.empty((weight.n, weight.k), dtype=dtype, device=weight.wq.device)
-    st = weight.struct()
+    st = weight._struct_ref()[1]
     _lib.check(_lib.lib().nf4_dequantize(ctypes.byref(st), _ptr(out), _DTYPES[dtype],
                                          _stream(stream)), "nf4_dequantize")
     return out
@@ -220,7 +225,7 @@ def nf4_dequantize_batch(weights, dtype=torch.bfloat16, outs=None, stream=None):
             outs = [torch.empty((w.n, w.k), dtype=dtype, device=w.wq.device) for w in weights]
     for o in outs:
         _need_cuda(o, "out")
-    structs = [w.struct() for w in weights]
+    structs = [w._struct_ref()[1] for w in weights]
     wptrs = (ctypes.POINTER(nf4_weight_t) * max(count, 1))(*[ctypes.pointer(s) for s in structs])
     optrs = (ctypes.c_void_p * max(count, 1))(*[o.data_ptr() for o in outs])
     _lib.check(_lib.lib().nf4_dequantize_batch(wptrs, count, optrs, _DTYPES[dtype], _stream(stream)),
@@ -270,7 +275,7 @@ def nf4_linear(X: torch.Tensor, weight: NF4Weight, dtype=torch.bfloat16,
     if out is None:
         with _memory_of(stream):
             out = torch.empty((m, weight.n), dtype=dtype, device=X.device)
-    st = weight.struct()
+    st = weight._struct_ref()[1]
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
     ws, ws_bytes = _ws(workspace)
@@ -315,7 +320,7 @@ def nf4_linear_group(X: torch.Tensor, weights, dtype=torch.bfloat16, outs=None,
     if outs is None:
         with _memory_of(stream):
             outs = [torch.empty((m, w.n), dtype=dtype, device=X.device) for w in weights]
-    structs = [w.struct() for w in weights]
+    structs = [w._struct_ref()[1] for w in weights]
     wptrs = (ctypes.POINTER(nf4_weight_t) * max(count, 1))(*[ctypes.pointer(s) for s in structs])
     yptrs = (ctypes.c_void_p * max(count, 1))(*[o.data_ptr() for o in outs])
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
@@ -339,7 +344,7 @@ def nf4_linear_dx(dY: torch.Tensor, weight: NF4Weight, dtype=torch.bfloat16,
     if out is None:
         with _memory_of(stream):
             out = torch.empty((m, weight.k), dtype=dtype, device=dY.device)
-    st = weight.struct()
+    st = weight._struct_ref()[1]
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
     _lib.check(_lib.lib().nf4_linear_dx(_ptr(dY), m, ctypes.byref(st), _ptr(out), _DTYPES[dtype], ds,
                                         _stream(stream)), "nf4_linear_dx")
@@ -373,7 +378,7 @@ def nf4_linear_lora(X: torch.Tensor, weight: NF4Weight, down: torch.Tensor, up: 
     if out is None:
         with _memory_of(stream):
             out = torch.empty((m, weight.n), dtype=dtype, device=X.device)
-    st = weight.struct()
+    st = weight._struct_ref()[1]
     ds = ctypes.c_void_p(0) if dev_status is None else _ptr(dev_status)
     flags = _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
     _lib.check(_lib.lib().nf4_linear_lora(_ptr(X), m, ctypes.byref(st), _ptr(down), _ptr(up), r, float(scale),
@@ -403,7 +408,7 @@ def nf4_merge_lora(weight: NF4Weight, down: torch.Tensor, up: torch.Tensor, scal
         if absmax is None:
             absmax = torch.empty(numel // 64, dtype=torch.float32, device=dev)
         w_new = torch.empty((weight.n, weight.k), dtype=torch.bfloat16, device=dev) if want_bf16 else None
-    st = weight.struct()
+    st = weight._struct_ref()[1]
     _lib.check(_lib.lib().nf4_merge_lora(ctypes.byref(st), _ptr(down), _ptr(up), r, float(scale),
                                          ctypes.c_void_p(0) if w_new is None else _ptr(w_new), _ptr(wq),
                                          _ptr(absmax), _stream(stream)), "nf4_merge_lora")
@@ -442,7 +447,7 @@ _GROUP_RULE = "k must be a multiple of 64, group 32 or a multiple of 64 that div
 
 
 @dataclass(frozen=True)
-class Int4Weight:
+class Int4Weight(_KeptStruct):
     """An integer 4-bit [n, k] weight with group scales: codes uint8 [n*k/2]
     (element 2i in the high nibble), ``scale`` [k/group, n] bf16 or fp32 and ``zero``
     uint8 [k/group, n], or None where every zero point is 8.  W ~ (q - zero) * scale."""
@@ -465,17 +470,12 @@ class Int4Weight:
         if zero is not None:
             _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
 
-    def _struct_ref(self):
-        return _kept_struct(self, (self.wq.data_ptr(), self.scale.data_ptr(), None if self.zero is None else self.zero.data_ptr()))
+    def _key(self):
+        return (self.wq.data_ptr(), self.scale.data_ptr(), None if self.zero is None else self.zero.data_ptr())
 
-    def struct(self) -> nf4_int4_weight_t:
-        return self._struct_ref()[1]
-
-    def _make(self, key):
+    def _make(self, key) -> nf4_int4_weight_t:
         return nf4_int4_weight_t(_lib.NF4_INT4_WEIGHT_MAGIC, _lib.NF4_WEIGHT_VERSION, self.n, self.k, self.group,
                                  _DTYPES[self.scale.dtype], 0, *key)
-
-    __getstate__ = _without_struct
 
     def nbytes(self) -> int:
         return (self.wq.numel() + self.scale.numel() * self.scale.element_size() +
