@@ -196,8 +196,6 @@ struct MoeWeight {
     int codebook = 0;
 };
 size_t moe_workspace_bytes(int64_t h, int64_t f, int E, int top);
-int moe_max_experts();
-int moe_max_top();
 cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, const MoeWeight& gate_up, const MoeWeight& down,
                        int top, bool renormalize, void* Y, int32_t* ids, float* probs, void* ws, const DeviceInfo& dev,
                        cudaStream_t stream);

@@ -27,6 +27,7 @@
 // of the result); integer codes are exact.  The activations a are kept in fp32 and, for the
 // products, rounded to fp16 (2^-11); where a token's largest one is outside [2^-6, 2^15)
 // they are read from the fp32 copy and scaled by a power of two on the way.
+#include "nf4.h"
 #include "nf4_few.cuh"
 #include "nf4_few_host.h"
 #include "nf4_ptx.cuh"
@@ -35,8 +36,10 @@ namespace nf4 {
 namespace moe {
 
 constexpr int kMaxM = 16;  // tokens of a pass
-constexpr int kMaxTop = 16;
-constexpr int kMaxE = 512;
+constexpr int kMaxTop = NF4_MOE_MAX_TOP_K;
+constexpr int kMaxE = NF4_MOE_MAX_EXPERTS;
+// choose: a lane a choice, sixteen logits a lane at most; route: a lane for each 32 experts
+static_assert(kMaxTop <= 32 && kMaxE <= 16 * 32 && kMaxE % 32 == 0, "routing tables");
 constexpr int kMaxPairs = kMaxM * kMaxTop;
 constexpr int kWarps = 20;  // 96 registers a thread; 16 and 24 warps took a few percent longer
 constexpr int kDepth = 3;  // steps on their way in a warp, beside the table of levels
@@ -542,8 +545,6 @@ static int form_of(const MoeWeight& w) {
 }  // namespace moe
 
 size_t moe_workspace_bytes(int64_t h, int64_t f, int E, int top) { return moe::layout(h, f, E, top).total; }
-int moe_max_experts() { return moe::kMaxE; }
-int moe_max_top() { return moe::kMaxTop; }
 
 cudaError_t launch_moe(const void* X, int64_t m, const void* router, int E, const MoeWeight& gate_up, const MoeWeight& down,
                        int top, bool renormalize, void* Y, int32_t* ids, float* probs, void* ws, const DeviceInfo& dev,

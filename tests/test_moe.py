@@ -1,11 +1,14 @@
 """The mixture-of-experts layer for a few tokens against its definition in 64 bits."""
 import ctypes
+import os
+import re
+import subprocess
 
 import pytest
 import torch
 
 from quantized_linear_layers_nf4_b200 import _lib
-from quantized_linear_layers_nf4_b200.build import build
+from quantized_linear_layers_nf4_b200.build import CSRC, INCLUDE, NVCC_FLAGS, build, nvcc
 
 gpu = pytest.mark.gpu
 FAKE = 0x10000
@@ -286,3 +289,15 @@ def test_binding_refusals(nf4):
         nf4.nf4_moe(x, r, gu, dn, 1, workspace=torch.empty(64, device="cuda", dtype=torch.uint8))
     with pytest.raises(nf4.NF4Error):
         nf4.nf4_moe(x[:0], r, gu, dn, 1)
+
+
+@pytest.mark.parametrize("limit", ["NF4_MOE_MAX_EXPERTS", "NF4_MOE_MAX_TOP_K"])
+def test_header_limits_are_those_of_the_routing_tables(tmp_path, limit):
+    """A header with a larger limit (its checks would let more through) does not build."""
+    header = open(os.path.join(INCLUDE, "nf4.h")).read()
+    value = int(re.search(r"#define %s (\d+)" % limit, header).group(1))
+    assert value == getattr(_lib, limit)
+    (tmp_path / "nf4.h").write_text(header.replace("#define %s %d" % (limit, value), "#define %s %d" % (limit, 4 * value)))
+    r = subprocess.run([nvcc(), "-I" + str(tmp_path), *NVCC_FLAGS, "-c", os.path.join(CSRC, "nf4_moe.cu"), "-o", str(tmp_path / "o.o")],
+                       capture_output=True, text=True)
+    assert r.returncode != 0 and "static assertion" in r.stderr and "routing tables" in r.stderr
