@@ -17,16 +17,11 @@
 // 4, over 28672 x 8192 27.4 us (4.4 TB/s, 69 % of the rate of a copy); sixteen tokens 42.4 us there,
 // bound by the issue of instructions (48.3 with groups of 64 and zero points).
 #include "nf4_few.cuh"
-#include "nf4_few_host.h"
+#include "nf4_int4_plan.h"
 #include "nf4_ptx.cuh"
 
 namespace nf4 {
 namespace int4 {
-
-constexpr int kWarps = 16;  // 128 registers a thread; 24 warps of 80 took a tenth longer
-
-// Steps on their way in a warp: sixteen tokens' X and sums leave room for three.
-constexpr int depth_of(int nt) { return nt == 1 ? 4 : 3; }
 
 struct GemvArgs {
     const __nv_bfloat16* x;
@@ -123,22 +118,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_int4_gemv(const __grid_const
     cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
-// Shared memory of a pass: X, the ring, sums of runs, and what is left for the CTA's sums.
-struct Room {
-    int64_t x_stride, x, ring, slots, left;
-};
-static Room room_of(int64_t m, int64_t k, int splits, int fmt, int warps) {
-    const int nt = m > 8 ? 2 : 1;
-    const int64_t all = (k + few::kStepK - 1) / few::kStepK;
-    Room r;
-    r.x_stride = (all + splits - 1) / splits * few::kStepK * 2 + (fmt == few::kG32 ? few::x_pad<few::kG32>() : few::x_pad<few::kG64>());
-    r.x = (m * r.x_stride + 127) / 128 * 128;
-    r.ring = static_cast<int64_t>(warps) * depth_of(nt) * few::kStepBytes;
-    r.slots = static_cast<int64_t>(warps) * nt * 512;
-    r.left = few::kMaxSmem - r.x - r.ring - r.slots;
-    return r;
-}
-
 }  // namespace int4
 
 static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early,
@@ -191,27 +170,19 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
     return few::launch(fn, clusters * splits, warps * 32, smem, splits, stream, args);
 }
 
-// Tokens of a pass: so many that an eighth of their X leaves room for 16 KB of sums (all sixteen
-// up to k = 26624, eight to 47104, then four).
-static int64_t tokens_of_pass(int64_t m, const Int4Args& w) {
-    int64_t most = kGemvMaxTokens;
-    while (most > 1 && int4::room_of(m < most ? m : most, w.k, 8, few::int4_format(w), int4::kWarps).left < 16 * 1024) most /= 2;
-    return most;
-}
-
 // A pass takes 7 us over 1024 x 4096, 9 over 4096 x 4096, 14 over 11008 x 4096, 42 over
 // 28672 x 8192 and 14 over 512 x 65536: 6 us, 3.2 TB/s and X.  The GEMM (int4_gemm_us) takes 14 us
 // over 4096 x 4096, 24 over 11008 x 4096 and 77 over 28672 x 8192 for any number of tokens up to 128.
 bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev) {
     if (m <= kGemvMaxTokens) return true;
     const double k = static_cast<double>(w.k), pass = 6.0 + static_cast<double>(w.n) * k * 0.5 / 3.2e6 + k * 5e-5;
-    const int64_t most = tokens_of_pass(m, w);
+    const int64_t most = int4::tokens_of_pass(m, w);
     return static_cast<double>((m + most - 1) / most) * pass < int4_gemm_us(m, w.n, w.k, dev);
 }
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,
                              cudaStream_t stream) {
-    const int64_t most = tokens_of_pass(m, w);
+    const int64_t most = int4::tokens_of_pass(m, w);
     for (int64_t t = 0; t < m; t += most) {
         const cudaError_t e = launch_int4_gemv_pass(static_cast<const char*>(X) + t * w.k * 2, m - t < most ? m - t : most, w,
                                                     static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, dev, stream);
