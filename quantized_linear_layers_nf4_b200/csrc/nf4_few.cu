@@ -23,7 +23,9 @@ cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& 
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     int n = dev.sm_count;
-    if (splits > 1) {
+    if (splits > dev.sm_count) {
+        n = 0;
+    } else if (splits > 1) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / splits * splits));
         cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -35,8 +37,12 @@ cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& 
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
-        if (e != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
+        if (e == cudaErrorInvalidClusterSize) {
+            cudaGetLastError();  // an answer, and none that a later launch should report
+            n = 0;
+        } else if (e != cudaSuccess) {
+            return e;
+        }
     }
     if (count < 1024) known[count++] = Known{fn, dev.device, splits, n};
     *out = n;

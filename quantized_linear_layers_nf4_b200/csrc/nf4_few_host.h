@@ -10,7 +10,8 @@ namespace few {
 constexpr int kMaxSmem = 216 * 1024;  // dynamic shared memory these kernels may ask for (beside some KB of static)
 
 // Clusters of `splits` (1, 2, 4, 8) CTAs, one CTA an SM, that the current device runs at
-// the same time; also allows the kernel its dynamic shared memory.  Asked of the runtime
+// the same time, 0 where it runs none of that size (a part of a GPU may have too few SMs
+// together); also allows the kernel its dynamic shared memory.  Asked of the runtime
 // once per kernel, device and size.
 cudaError_t resident(const void* fn, int threads, int splits, const DeviceInfo& dev, int* out);
 

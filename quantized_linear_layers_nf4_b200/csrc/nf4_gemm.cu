@@ -31,7 +31,7 @@
 // Integer codes (kInt4) take the same way with three differences.  Two teams of eight decoding
 // warps take the stages in turn, since a warp spends most of a stage waiting; a tile has 32 to 256
 // weight rows and k is split over a cluster of up to 8 CTAs, as the number of tiles asks
-// (plan_int4), the threads of a team share a small tile's rows, and the CTAs' sums are added in rank
+// (plan_int4 in nf4_int4_plan.h), the threads of a team share a small tile's rows, and the CTAs' sums are added in rank
 // order through distributed shared memory; and up to 128 tokens only half of the token tile is
 // multiplied.  512 tokens over 11008 x 4096 take 45 us (1026 TFLOP/s; with one team and 256 rows 60),
 // 128 over 4096 x 4096 14 us.  A stage takes 750 to 1300 cycles, of which the MMAs are 128 to 1024: bound by what a
@@ -43,7 +43,7 @@
 
 #include "nf4_common.cuh"
 #include "nf4_decode.cuh"
-#include "nf4_few_host.h"
+#include "nf4_int4_plan.h"
 #include "nf4_internal.h"
 #include "nf4_ptx.cuh"
 #include "nf4_tmap.h"
@@ -51,26 +51,13 @@
 namespace nf4 {
 namespace gemm {
 
-constexpr int kBM = 256;  // tokens per CTA tile (two 128-row MMA halves)
-constexpr int kBN = 256;  // weight rows per CTA tile (MMA N)
-constexpr int kBK = 64;   // k per stage: one 128-byte swizzle row of bf16
-constexpr int kStagesA = 3;
-constexpr int kStagesB = 2;
-constexpr int kStagesP = 4;
-constexpr int kABytes = kBM * kBK * 2;  // 32768
-constexpr int kBBytes = kBN * kBK * 2;  // 32768
-constexpr int kPBytes = kBN * kBK / 2;  // 8192
 constexpr int kDequantWarps = 8;
 constexpr int kThreads = 32 * (4 + kDequantWarps);
 constexpr int kInt4F32 = 4;
-constexpr int kPartPad = 4;  // words between the rows of a CTA's sums in shared memory, for the banks
 // A decoding warp spends more of a stage waiting than working: two teams of them take turns for integer
 // codes, whose decoding needs few enough registers.
 constexpr int threads_of(int integer) { return integer ? kThreads + 32 * kDequantWarps : kThreads; }
 constexpr uint32_t kTmemCols = 512;
-constexpr int kOffB = kStagesA * kABytes;
-constexpr int kOffP = kOffB + kStagesB * kBBytes;
-constexpr int kOffBar = kOffP + kStagesP * kPBytes;
 constexpr int kNumBars = 2 * kStagesA + 2 * kStagesB + 2 * kStagesP + 4;  // + low-rank tiles, MMA drain
 constexpr int kSmemBytes = 1024 + kOffBar + kNumBars * 8 + 16;
 
@@ -828,32 +815,11 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Tiles for integer codes.  A stage takes a time that goes about as 350 + its weight rows, since
-// most of it is the decoding warps' latency, so that a few large tiles with k split over a cluster
-// beat many small ones, and the waves of tiles over the SMs go in whole numbers.  128 tokens over
-// 4096 x 4096 take 14 us with 256 rows and k in eight parts, 25 with 32 rows and k whole, 44 with 256
-// and whole; 512 over 11008 x 4096, whose tiles leave no SMs for parts, 45 with 160 rows and 59 with 256.
-struct Plan {
-    int rows, splits;
-    double us;
-};
-cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev, Plan* out) {
-    const int64_t token_tiles = (m + kBM - 1) / kBM, stages = k / kBK, x_rows = m <= 128 ? 128 : kBM;
-    const double stage = 0.95e-3 * (m <= 128 ? 1.0 : 1.15);
-    *out = Plan{kBN, 1, 1e30};
-    for (int splits = 1; splits == 1 || (splits <= 8 && stages >= 4 * splits); splits *= 2) {
-        int fit = 0;  // clusters at a time
-        const cudaError_t e = few::resident(reinterpret_cast<const void*>(&k_nf4_gemm<true, false, 1>), threads_of(1), splits, dev, &fit);
-        if (e != cudaSuccess) return e;
-        for (int rows = kBN; rows >= 32; rows -= 32) {
-            if (splits > 1 && x_rows * (rows + kPartPad) * 4 > kOffBar) continue;
-            const int64_t waves = ((n + rows - 1) / rows * token_tiles + fit - 1) / fit;
-            double us = 5.0 + stage * static_cast<double>(waves * ((stages + splits - 1) / splits) * (350 + rows));
-            if (splits > 1) us += 1.5 + 3e-5 * static_cast<double>(x_rows * rows * waves);
-            if (us < out->us) *out = Plan{rows, splits, us};
-        }
-    }
-    return cudaSuccess;
+static cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev, Plan* out) {
+    auto fit = [&](int splits, int* clusters) {
+        return few::resident(reinterpret_cast<const void*>(&k_nf4_gemm<true, false, 1>), threads_of(1), splits, dev, clusters);
+    };
+    return plan_int4(m, n, k, fit, out);
 }
 
 }  // namespace gemm

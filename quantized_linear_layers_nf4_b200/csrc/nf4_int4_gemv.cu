@@ -120,54 +120,47 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_int4_gemv(const __grid_const
 
 }  // namespace int4
 
-static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early,
-                                         const DeviceInfo& dev, cudaStream_t stream) {
+static const void* gemv_kernel(int64_t m, const Int4Args& w) {
     using namespace int4;
-    const int nt = m > 8 ? 2 : 1;
-    const int fmt = few::int4_format(w);
 #define NF4_INT4_GEMV(F, Z) reinterpret_cast<const void*>(&k_int4_gemv<F, Z, 1>), reinterpret_cast<const void*>(&k_int4_gemv<F, Z, 2>)
     static const void* const fns[12] = {NF4_INT4_GEMV(few::kG128, false), NF4_INT4_GEMV(few::kG128, true),
                                         NF4_INT4_GEMV(few::kG64, false),  NF4_INT4_GEMV(few::kG64, true),
                                         NF4_INT4_GEMV(few::kG32, false),  NF4_INT4_GEMV(few::kG32, true)};
 #undef NF4_INT4_GEMV
-    const void* fn = fns[(fmt - few::kG128) * 4 + (w.zero ? 2 : 0) + nt - 1];
-    const int64_t all = (w.k + few::kStepK - 1) / few::kStepK;
-    const int64_t groups = (w.n + 7) / 8;
+    return fns[(few::int4_format(w) - few::kG128) * 4 + (w.zero ? 2 : 0) + (m > 8 ? 1 : 0)];
+}
 
-    GemvArgs a = {};
-    // k is split over a cluster where a CTA's share of X would take long to bring in (64 KB),
-    // or where there are fewer row groups than SMs and each part still feeds the warps
-    int splits = 1;
-    while (splits < 8 && (m * w.k * 2 / splits > 64 * 1024 || (groups * splits * 2 <= dev.sm_count && all >= splits * kWarps))) splits *= 2;
-    int fit = 0;
-    cudaError_t e = few::resident(fn, kWarps * 32, splits, dev, &fit);
+static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, int widest,
+                                         const DeviceInfo& dev, cudaStream_t stream) {
+    using namespace int4;
+    const void* fn = gemv_kernel(m, w);
+    Pass p;
+    const cudaError_t e = plan_pass(m, w, dev.sm_count, widest, [&](int splits, int* n) { return few::resident(fn, kWarps * 32, splits, dev, n); }, &p);
     if (e != cudaSuccess) return e;
-    int64_t clusters = fit < groups ? fit : groups;
-    const int64_t steps = ((groups + clusters - 1) / clusters + 1) / 2 * ((all + splits - 1) / splits);
-    // m = 4 is about where what a warp costs at its start outweighs what it adds
-    const int warps = steps <= (m > 4 ? 1 : 2) * few::kFewSteps && m <= kWarps / 2 ? kWarps / 2 : kWarps;  // a warp or more a token for X
-    const Room at = room_of(m, w.k, splits, fmt, warps);
-    if (at.left < m * 64) return cudaErrorInvalidConfiguration;
-    while (splits > 1 && (groups + clusters - 1) / clusters * 8 * m * 4 > at.left) clusters += fit;
-    if (clusters * splits > 0x7fffffff || groups > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    GemvArgs a = {};
     a.x = reinterpret_cast<const __nv_bfloat16*>(X);
     a.w = few::int4_weight(w);
     a.y = Y;
     a.m = static_cast<int>(m);
-    while ((2 << a.x_lg) * m <= warps) ++a.x_lg;
-    a.rows = few::shares_of(static_cast<int>(groups), static_cast<int>(clusters));
-    a.ks = few::shares_of(static_cast<int>(all), splits);
-    a.splits = splits;
-    a.x_stride = static_cast<int>(at.x_stride);
-    a.ring_at = static_cast<int>(at.x);
-    a.slots_at = static_cast<int>(at.x + at.ring);
-    a.part_at = static_cast<int>(at.x + at.ring + at.slots);
-    a.part_rows = static_cast<int>((groups + clusters - 1) / clusters * 8);
+    while ((2 << a.x_lg) * m <= p.warps) ++a.x_lg;
+    a.rows = few::shares_of(static_cast<int>(p.groups), static_cast<int>(p.clusters));
+    a.ks = few::shares_of(static_cast<int>(p.steps), p.splits);
+    a.splits = p.splits;
+    a.x_stride = static_cast<int>(p.at.x_stride);
+    a.ring_at = static_cast<int>(p.at.x);
+    a.slots_at = static_cast<int>(p.at.x + p.at.ring);
+    a.part_at = static_cast<int>(p.at.x + p.at.ring + p.at.slots);
+    a.part_rows = static_cast<int>((p.groups + p.clusters - 1) / p.clusters * 8);
     a.bf16_out = y_bf16 ? 1 : 0;
     a.early = early ? 1 : 0;
-    const size_t smem = static_cast<size_t>(a.part_at + (splits > 1 ? m * a.part_rows * 4 : 0));
+    const size_t smem = static_cast<size_t>(a.part_at + (p.splits > 1 ? m * a.part_rows * 4 : 0));
     void* args[1] = {&a};
-    return few::launch(fn, clusters * splits, warps * 32, smem, splits, stream, args);
+    return few::launch(fn, p.clusters * p.splits, p.warps * 32, smem, p.splits, stream, args);
+}
+
+static cudaError_t widest_of(int64_t m, const Int4Args& w, const DeviceInfo& dev, int* widest) {
+    const void* fn = gemv_kernel(m, w);
+    return int4::widest_cluster([&](int splits, int* n) { return few::resident(fn, int4::kWarps * 32, splits, dev, n); }, widest);
 }
 
 // A pass takes 7 us over 1024 x 4096, 9 over 4096 x 4096, 14 over 11008 x 4096, 42 over
@@ -176,16 +169,21 @@ static cudaError_t launch_int4_gemv_pass(const void* X, int64_t m, const Int4Arg
 bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev) {
     if (m <= kGemvMaxTokens) return true;
     const double k = static_cast<double>(w.k), pass = 6.0 + static_cast<double>(w.n) * k * 0.5 / 3.2e6 + k * 5e-5;
-    const int64_t most = int4::tokens_of_pass(m, w);
+    int widest = 1;
+    if (widest_of(m, w, dev, &widest) != cudaSuccess) return false;
+    const int64_t most = int4::tokens_of_pass(m, w, widest);
     return static_cast<double>((m + most - 1) / most) * pass < int4_gemm_us(m, w.n, w.k, dev);
 }
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,
                              cudaStream_t stream) {
-    const int64_t most = int4::tokens_of_pass(m, w);
+    int widest = 1;
+    const cudaError_t found = widest_of(m, w, dev, &widest);
+    if (found != cudaSuccess) return found;
+    const int64_t most = int4::tokens_of_pass(m, w, widest);
     for (int64_t t = 0; t < m; t += most) {
         const cudaError_t e = launch_int4_gemv_pass(static_cast<const char*>(X) + t * w.k * 2, m - t < most ? m - t : most, w,
-                                                    static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, dev, stream);
+                                                    static_cast<char*>(Y) + t * w.n * (y_bf16 ? 2 : 4), y_bf16, early, widest, dev, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
