@@ -526,10 +526,14 @@ nf4_status_t nf4_int4_dequantize(const nf4_int4_weight_t* w, void* out, nf4_dtyp
  * in fp32, and the scale multiplies the sum of each group's part of 128 columns:
  * What = (q - z) s is never rounded.  (X goes through fp16 times a power of two per
  * token and range of columns, which keeps every bit of values down to 2^-31 of the
- * range's largest; smaller ones lose bits.)  For many tokens the weight is restored
- * to bf16 on chip, What = bf16_round(fp32((q - z) s)), and runs on the dequant-GEMM of
- * nf4_linear.  Up to 16 tokens are few; above, the path that is expected to be faster
- * for m, n, k and the device's number of SMs.  Sums are in fp32 in an order that does
+ * range's largest; smaller ones lose bits.  With scales of 2^93 or more its sums may
+ * overflow where the result would not.)  For many tokens the weight is restored
+ * on chip and runs on the dequant-GEMM of nf4_linear: with y_dtype NF4_BF16 as
+ * What = bf16_round(fp32((q - z) s)), with NF4_F32 as the sum of two bf16 values, which is
+ * (q - z) s itself for bf16 scales and within 2^-17 of it for fp32 ones.  Up to 16 tokens
+ * are few; above, the path that is expected to be faster for m, n, k, y_dtype and the
+ * device's number of SMs: which one it is shows in a bf16 result by the rounding of the
+ * weight, and not in an fp32 one beyond that 2^-17.  Sums are in fp32 in an order that does
  * not depend on timing.
  *   X          device, bf16 [m, k], 16-byte aligned
  *   m          rows of X (tokens), >= 1

@@ -544,8 +544,9 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
                     flags: int = 0) -> torch.Tensor:
     """Y = X @ W_hat^T for bf16 X [m, k] and an integer 4-bit weight; Y [m, n] in
     ``dtype`` (in that of ``out``, where given).  For few tokens (up to 16, and more
-    where that is faster) the weight is not rounded; otherwise it is restored to bf16
-    on chip, as in nf4_linear.
+    where that is faster) the weight is not rounded; otherwise it is restored on chip, to
+    bf16 as in nf4_linear for a bf16 result and to twice that precision for an fp32 one
+    (which takes up to 1.7 times as long).
     ``weights_early`` and ``flags`` as for nf4_linear."""
     _need_cuda(X, "X")
     dev = X.device

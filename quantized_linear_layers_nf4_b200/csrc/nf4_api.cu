@@ -450,7 +450,7 @@ nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* 
     nf4::DeviceInfo dev;
     if ((st = device_ok(&dev)) != NF4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!test && nf4::int4_few_tokens(m, a, dev))
+    if (!test && nf4::int4_few_tokens(m, a, y_dtype == NF4_BF16, dev))
         return from_cuda(nf4::launch_int4_gemv(X, m, a, Y, y_dtype == NF4_BF16, (flags & NF4_LINEAR_WEIGHTS_EARLY) != 0, dev, s));
     return from_cuda(nf4::launch_gemm(X, m, a.wq, nullptr, nullptr, nullptr, a.n, a.k, Y, y_dtype == NF4_BF16, dev_status,
                                       nf4::LoraArgs(), 0, test ? nf4::kTestStall : 0u, dev, s, &a));

@@ -64,20 +64,40 @@ struct Planes {
     uint32_t h[4], l[4];
 };
 
+// Byte planes of a table from its pairs of entries, t[j] = {T[2j] low half, T[2j+1] high half}.
+__device__ __forceinline__ void split_planes(const uint32_t (&t)[8], Planes& P) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        P.h[q] = prmt(t[2 * q], t[2 * q + 1], 0x7531);
+        P.l[q] = prmt(t[2 * q], t[2 * q + 1], 0x6420);
+    }
+}
+
 // T[i] = bf16(fp32(c_i * a)) for the 16 levels (pairs of levels multiplied by
 // one packed f32x2 multiply), split into byte planes.
 __device__ __forceinline__ void build_planes(const uint64_t (&cpair)[8], float a, Planes& P) {
     const uint64_t aa = dup_f32x2(a);
     uint32_t t[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = scale_pack(cpair[j], aa);
-    // scale_pack puts the first level of a pair in the low half, so t[j] =
-    // {T[2j] low half, T[2j+1] high half}
+    for (int j = 0; j < 8; ++j) t[j] = scale_pack(cpair[j], aa);  // the first level of a pair goes to the low half
+    split_planes(t, P);
+}
+
+// What that leaves of the products: T[i] = bf16(v - bf16(v)), v = fp32(c_i * a), 0 where v is not finite.
+__device__ __forceinline__ void build_planes_rest(const uint64_t (&cpair)[8], float a, Planes& P) {
+    const uint64_t aa = dup_f32x2(a);
+    uint32_t t[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        P.h[q] = prmt(t[2 * q], t[2 * q + 1], 0x7531);
-        P.l[q] = prmt(t[2 * q], t[2 * q + 1], 0x6420);
+    for (int j = 0; j < 8; ++j) {
+        uint64_t v;
+        float lo, hi;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(cpair[j]), "l"(aa));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+        lo = __fsub_rn(lo, __bfloat162float(__float2bfloat16_rn(lo)));
+        hi = __fsub_rn(hi, __bfloat162float(__float2bfloat16_rn(hi)));
+        t[j] = pack_bf16x2(fabsf(lo) < __int_as_float(0x7f800000) ? lo : 0.0f, fabsf(hi) < __int_as_float(0x7f800000) ? hi : 0.0f);
     }
+    split_planes(t, P);
 }
 
 // Four nibbles (the low 16 bits of s; s ^ 0x8888 in sx) -> two bf16x2 words in

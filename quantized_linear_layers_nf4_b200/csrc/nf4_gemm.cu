@@ -78,7 +78,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // A word's eight integer codes as bf16((q - z) s), pairs in k order.  A nibble in the low bits
 // of 128's mantissa is 128 + q; less z2 = 128 + z it is q - z, exact, and the product of that
 // with a bf16 scale (s2: twice) is exact before its one rounding, so these are the values
-// that nf4_int4_dequantize writes.
+// that nf4_int4_dequantize writes.  kRest: what that rounding took off, exact as well (a product has
+// twelve bits at most, eight are kept).
+template <bool kRest>
 __device__ __forceinline__ void int4_bf16(uint32_t w, uint32_t z2, uint32_t s2, uint32_t (&o)[4]) {
     const uint32_t v = w >> 4;
 #pragma unroll
@@ -87,6 +89,7 @@ __device__ __forceinline__ void int4_bf16(uint32_t w, uint32_t z2, uint32_t s2, 
         uint32_t d;
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(few::and_or(p, 0x000f000fu, 0x43004300u)), "r"(z2));
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(d), "r"(s2));
+        if (kRest) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(d), "r"(s2), "r"(o[i] ^ 0x80008000u));
     }
 }
 
@@ -95,6 +98,11 @@ __device__ __forceinline__ void int4_bf16(uint32_t w, uint32_t z2, uint32_t s2, 
 // one permute, one logic and two packed bf16 operations (half the integer pipe's work of the
 // table, which bounds the kernel); with fp32 scales a group has a 16-entry
 // table bf16(fp32((j - z) s)) as a codebook's block has.  Everything else is the same.
+// Where Y is fp32 (kParts = 2), a weight is the sum of two bf16 values, as the few-token kernel's results
+// are those of the unrounded weight: a stage's X is multiplied by the rounded weights, which one team
+// decodes, and by what the rounding left, which the other does from the same codes.  The sum is exact
+// with bf16 scales, and with fp32 ones off by 2^-17 at most.  512 tokens over 11008 x 4096 take 87 us
+// replayed from a graph (bf16 results 45), 128 over 4096 x 4096 20 us (14).
 template <bool kBf16Out, bool kLora, int kInt4>
 __global__ void __launch_bounds__(threads_of(kInt4), 1)
 k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -128,6 +136,8 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
     const int halves = kInt4 && m - m0 <= 128 ? 1 : 2;  // of the token tile that hold any
     // k over the CTAs of a cluster: this one has stages k0 .. k0 + nk
     const few::Shares parts = few::shares_of(static_cast<int>(k / kBK), kInt4 ? splits : 1);
+    constexpr int kParts = kInt4 && !kBf16Out ? 2 : 1;  // of a weight
+    static_assert(kParts == 1 || kParts == kStagesB, "a part has one stage");
     const int rank = kInt4 ? static_cast<int>(blockIdx.z) : 0, k0 = parts.start(rank);
     const int nk = parts.start(rank + 1) - k0;
     const uint32_t sbase = smem_u32(smem);
@@ -143,7 +153,7 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         }
         for (int s = 0; s < kStagesP; ++s) {
             mbar_init(&full_p[s], 1);
-            mbar_init(&empty_p[s], kDequantWarps);
+            mbar_init(&empty_p[s], kParts * kDequantWarps);
         }
         mbar_init(acc_ready, 1);
         mbar_init(drained, 1);
@@ -210,26 +220,31 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
         const uint32_t idesc = kInt4 ? (kIdesc & ~(0x3fu << 17)) | static_cast<uint32_t>(bn >> 3) << 17 : kIdesc;
         for (int kt = 0; kt < nk; ++kt) {
             const int sa = kt % kStagesA;
-            const int sb = kt % kStagesB;
-            if (!__all_sync(kFull, mbar_wait_n(&full_a[sa], (kt / kStagesA) & 1, lim) &&
-                                       mbar_wait_n(&full_b[sb], (kt / kStagesB) & 1, lim))) {
-                timed_out = true;
-                break;
-            }
-            tc_fence_after();
-            const uint64_t a_desc = smem_desc_sw128(sbase + sa * kABytes), b_desc = smem_desc_sw128(sbase + kOffB + sb * kBBytes);
-            if (leader) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (kInt4 && h == halves) break;
-#pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j)  // a descriptor counts 16 bytes
-                        tc_mma_bf16(tmem + h * 256, a_desc + h * (128 * 128 / 16) + 2 * j, b_desc + 2 * j, idesc, (kt > 0 || j > 0) ? 1u : 0u);
+            for (int part = 0; part < kParts; ++part) {
+                const int sb = kParts == 1 ? kt % kStagesB : part, turn = kParts == 1 ? kt / kStagesB : kt;
+                if (!__all_sync(kFull, (part > 0 || mbar_wait_n(&full_a[sa], (kt / kStagesA) & 1, lim)) &&
+                                           mbar_wait_n(&full_b[sb], turn & 1, lim))) {
+                    timed_out = true;
+                    break;
                 }
-                tc_commit(&empty_a[sa]);
-                tc_commit(&empty_b[sb]);
+                tc_fence_after();
+                const uint64_t a_desc = smem_desc_sw128(sbase + sa * kABytes), b_desc = smem_desc_sw128(sbase + kOffB + sb * kBBytes);
+                if (leader) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (kInt4 && h == halves) break;
+#pragma unroll
+                        for (int j = 0; j < kBK / 16; ++j)  // a descriptor counts 16 bytes
+                            tc_mma_bf16(tmem + h * 256, a_desc + h * (128 * 128 / 16) + 2 * j, b_desc + 2 * j, idesc,
+                                        (kt > 0 || part > 0 || j > 0) ? 1u : 0u);
+                    }
+                    if (part == kParts - 1) tc_commit(&empty_a[sa]);
+                    tc_commit(&empty_b[sb]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (timed_out) break;
         }
         if (leader) {
             if (kLora && lora_tc && !timed_out) {
@@ -269,7 +284,8 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
     } else if (warp >= 4) {
         // ------------------------ dequantize, then epilogue --------------------
         // weight row of the tile; where that has few, two, four or eight threads share one
-        constexpr int kTeams = kInt4 ? 2 : 1;  // of decoding warps, which take stages in turn
+        constexpr int kTeams = kInt4 ? 2 : 1;  // of decoding warps, which take stages in turn, or a part of each
+        constexpr int kTurn = kTeams / kParts;  // stages from one of a team's to its next
         const int share = (kInt4 == 0 || bn > 128) ? 0 : (bn > 64 ? 1 : (bn > 32 ? 2 : 3));
         const int team = kInt4 ? (warp - 4) / kDequantWarps : 0, local = threadIdx.x - 128 - team * 32 * kDequantWarps;
         const int part = kInt4 ? local / bn : 0;  // one in a warp
@@ -329,16 +345,16 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
             }
         };
         if (kInt4) {
-            const int first = k0 + team;
+            const int first = k0 + (kParts == 1 ? team : 0);
             const int before = kGroups == 2 ? 2 * first : first / sides.per;
             gleft -= first - before * sides.per;
             s_at += before * kScale * n;
             z_at += before * z_row;
-            if (team < nk) fetch_sides();
+            if (first < k0 + nk) fetch_sides();
         }
-        for (int kt = team; kt < nk; kt += kTeams) {
+        for (int kt = kParts == 1 ? team : 0; kt < nk; kt += kTurn) {
             const int sp = kt % kStagesP;
-            const int sb = kt % kStagesB;
+            const int sb = kParts == 1 ? kt % kStagesB : team, turn = kParts == 1 ? kt / kStagesB : kt;
             int q = 0;
             float sc = 0.0f;
             uint32_t iscale[kGroups], izero[kGroups];
@@ -348,8 +364,8 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                     iscale[i] = gs[i];
                     izero[i] = gz[i] & 15u;
                 }
-                if (kt + kTeams < nk) {
-                    later(kTeams);
+                if (kt + kTurn < nk) {
+                    later(kTurn);
                     fetch_sides();
                 }
             } else if (grouped) {
@@ -382,13 +398,14 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                 uint64_t lev[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lev[j]) : "l"(cpair[j]), "l"(off));
-                build_planes(lev, __uint_as_float(iscale[i]), P);
+                if (kParts == 2 && team) build_planes_rest(lev, __uint_as_float(iscale[i]), P);
+                else build_planes(lev, __uint_as_float(iscale[i]), P);
             };
             constexpr bool pairs = kInt4 && !kF32;
             if (pairs) {
             } else if (kInt4) int4_planes(0);
             else build_planes(cpair, absmax_hat(q, sc, mu), P);
-            if (kt >= kStagesB && !__all_sync(kFull, mbar_wait_n(&empty_b[sb], ((kt / kStagesB) - 1) & 1, lim))) {
+            if (turn > 0 && !__all_sync(kFull, mbar_wait_n(&empty_b[sb], (turn - 1) & 1, lim))) {
                 timed_out = true;
                 break;
             }
@@ -401,14 +418,20 @@ k_nf4_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUt
                 for (int i = 0; i < kGroups; ++i) {
                     z2[i] = izero[i] * 0x10001u + 0x43004300u;
                     s2[i] = iscale[i] * 0x10001u;
+                    // nothing is left of a product that is not finite
+                    if (kParts == 2 && team && (iscale[i] & 0x7f80u) == 0x7f80u) s2[i] = 0u;
                 }
+                auto words = [&](auto&& decoded) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if ((c << share) >> 3 != part) continue;
-                    uint32_t o[4];
-                    int4_bf16(w[c], z2[kGroups * c / 8], s2[kGroups * c / 8], o);
-                    sts128(bst + ((c ^ swz) << 4), o[0], o[1], o[2], o[3]);
-                }
+                    for (int c = 0; c < 8; ++c) {
+                        if ((c << share) >> 3 != part) continue;
+                        uint32_t o[4];
+                        decoded(w[c], z2[kGroups * c / 8], s2[kGroups * c / 8], o);
+                        sts128(bst + ((c ^ swz) << 4), o[0], o[1], o[2], o[3]);
+                    }
+                };
+                if (kParts == 2 && team) words(int4_bf16<true>);
+                else words(int4_bf16<false>);
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -815,11 +838,11 @@ k_nf4_gemm_dx(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-static cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev, Plan* out) {
+static cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, bool y_bf16, const DeviceInfo& dev, Plan* out) {
     auto fit = [&](int splits, int* clusters) {
         return few::resident(reinterpret_cast<const void*>(&k_nf4_gemm<true, false, 1>), threads_of(1), splits, dev, clusters);
     };
-    return plan_int4(m, n, k, fit, out);
+    return plan_int4(m, n, k, y_bf16 ? 1 : 2, fit, out);
 }
 
 }  // namespace gemm
@@ -865,7 +888,7 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
     const int x_rows = w4 && m <= 128 ? 128 : gemm::kBM;
     gemm::Plan plan = {gemm::kBN, 1, 0.0};
     if (w4) {
-        const cudaError_t pe = gemm::plan_int4(m, n, k, dev, &plan);
+        const cudaError_t pe = gemm::plan_int4(m, n, k, y_bf16, dev, &plan);
         if (pe != cudaSuccess) return pe;
     }
     const int bn = plan.rows;
@@ -930,9 +953,9 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
     return e;
 }
 
-double int4_gemm_us(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev) {
+double int4_gemm_us(int64_t m, int64_t n, int64_t k, bool y_bf16, const DeviceInfo& dev) {
     gemm::Plan plan = {};
-    return gemm::plan_int4(m, n, k, dev, &plan) == cudaSuccess ? plan.us : 1e30;
+    return gemm::plan_int4(m, n, k, y_bf16, dev, &plan) == cudaSuccess ? plan.us : 1e30;
 }
 
 cudaError_t launch_gemm_dx(const void* dY, int64_t m, const uint8_t* wq, const int8_t* absmax_q,

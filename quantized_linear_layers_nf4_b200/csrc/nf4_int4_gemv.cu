@@ -166,13 +166,13 @@ static cudaError_t widest_of(int64_t m, const Int4Args& w, const DeviceInfo& dev
 // A pass takes 7 us over 1024 x 4096, 9 over 4096 x 4096, 14 over 11008 x 4096, 42 over
 // 28672 x 8192 and 14 over 512 x 65536: 6 us, 3.2 TB/s and X.  The GEMM (int4_gemm_us) takes 14 us
 // over 4096 x 4096, 24 over 11008 x 4096 and 77 over 28672 x 8192 for any number of tokens up to 128.
-bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev) {
+bool int4_few_tokens(int64_t m, const Int4Args& w, bool y_bf16, const DeviceInfo& dev) {
     if (m <= kGemvMaxTokens) return true;
     const double k = static_cast<double>(w.k), pass = 6.0 + static_cast<double>(w.n) * k * 0.5 / 3.2e6 + k * 5e-5;
     int widest = 1;
     if (widest_of(m, w, dev, &widest) != cudaSuccess) return false;
     const int64_t most = int4::tokens_of_pass(m, w, widest);
-    return static_cast<double>((m + most - 1) / most) * pass < int4_gemm_us(m, w.n, w.k, dev);
+    return static_cast<double>((m + most - 1) / most) * pass < int4_gemm_us(m, w.n, w.k, y_bf16, dev);
 }
 
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early, const DeviceInfo& dev,

@@ -112,9 +112,9 @@ struct Plan {
     double us;
 };
 template <typename Fit>
-cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, Fit&& fit_of, Plan* out) {
+cudaError_t plan_int4(int64_t m, int64_t n, int64_t k, int parts, Fit&& fit_of, Plan* out) {
     const int64_t token_tiles = (m + kBM - 1) / kBM, stages = k / kBK, x_rows = m <= 128 ? 128 : kBM;
-    const double stage = 0.95e-3 * (m <= 128 ? 1.0 : 1.15);
+    const double stage = 0.95e-3 * (m <= 128 ? 1.0 : 1.15) * parts;
     *out = Plan{kBN, 1, 1e30};
     for (int splits = 1; splits == 1 || (splits <= 8 && stages >= 4 * splits); splits *= 2) {
         int fit = 0;  // clusters at a time

@@ -177,9 +177,9 @@ cudaError_t launch_gemm(const void* X, int64_t m, const uint8_t* wq, const int8_
 cudaError_t launch_int4_quantize(const void* W, bool w_bf16, int64_t n, int64_t k, int64_t group, uint8_t* wq, void* scale,
                                  bool scale_f32, uint8_t* zero, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_int4_dequantize(const Int4Args& w, void* out, bool out_bf16, const DeviceInfo& dev, cudaStream_t stream);
-double int4_gemm_us(int64_t m, int64_t n, int64_t k, const DeviceInfo& dev);  // the GEMM's time, about
+double int4_gemm_us(int64_t m, int64_t n, int64_t k, bool y_bf16, const DeviceInfo& dev);  // the GEMM's time, about
 // Whether m tokens take the few-token kernel, in passes of kGemvMaxTokens, rather than the GEMM.
-bool int4_few_tokens(int64_t m, const Int4Args& w, const DeviceInfo& dev);
+bool int4_few_tokens(int64_t m, const Int4Args& w, bool y_bf16, const DeviceInfo& dev);
 // With `early` the weight is read before the preceding kernel is waited for.
 cudaError_t launch_int4_gemv(const void* X, int64_t m, const Int4Args& w, void* Y, bool y_bf16, bool early,
                              const DeviceInfo& dev, cudaStream_t stream);

@@ -82,3 +82,54 @@ def test_integers_are_exact(nf4, size, tile, group, scale, zero):
     want = x.double() @ nf4.nf4_int4_dequantize(w, torch.float32).double().t()
     assert torch.equal(nf4.nf4_int4_linear(x, w, torch.float32).double(), want)
     assert torch.equal(nf4.nf4_int4_linear(x, w), want.bfloat16())
+
+
+@gpu
+@pytest.mark.parametrize("group,k", [(32, 512), (64, 512), (128, 512), (512, 512), (192, 576), (320, 640)])
+@pytest.mark.parametrize("scale", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("n", [1003, 4100])
+def test_fp32_results_keep_the_weight(nf4, group, k, scale, zero, n):
+    """With fp32 results a weight is two bf16 values.  The first is off by half a step of 2^-8 of the power
+    of two below it at most; the rest has twelve bits less eight with a bf16 scale, which are kept,
+    and is itself rounded with an fp32 one, by half a step of a value 2^-8 as large: 2^-17."""
+    w = _weight(nf4, n, k, group, zero, _any_scale(scale), group + n)
+    want = nf4.nf4_int4_dequantize(w, torch.float32).t()
+    x = torch.eye(k, device="cuda").bfloat16()
+    for y in (nf4.nf4_int4_linear(x, w, torch.float32), torch.cat([nf4.nf4_int4_linear(x[c:c + 100], w, torch.float32) for c in range(0, k, 100)])):
+        if scale == torch.bfloat16:
+            assert torch.equal(y, want)
+        else:
+            assert torch.all((y.double() - want.double()).abs() <= 2.0 ** -17 * want.double().abs())
+
+
+@gpu
+@pytest.mark.parametrize("m,n,k,group", [(300, 1003, 5184, 32), (130, 2048, 2048, 128), (40, 257, 8192, 64), (512, 4096, 4096, 128), (20, 96, 1024, 256)])
+@pytest.mark.parametrize("scale", [torch.bfloat16, torch.float32])
+def test_fp32_results_of_any_weight(nf4, m, n, k, group, scale):
+    """Two products a weight, each sum off by 2^-23 of the magnitudes so far, and what the weight has lost."""
+    w = _weight(nf4, n, k, group, True, _any_scale(scale), k)
+    w64 = nf4.nf4_int4_dequantize(w, torch.float32).double()
+    x = torch.randn(m, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(n)).bfloat16()
+    ref, mag = x.double() @ w64.t(), x.double().abs() @ w64.abs().t()
+    tol = 2 * k * 2.0 ** -23 * mag * (1 + 2.0 ** -7) + (2.0 ** -17 + 2.0 ** -24 if scale == torch.float32 else 0.0) * mag
+    assert torch.all((nf4.nf4_int4_linear(x, w, torch.float32).double() - ref).abs() <= tol)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [torch.bfloat16, torch.float32])
+def test_scales_that_are_not_finite(nf4, scale):
+    """An infinite or NaN scale: the rows that have it are infinite or NaN as a sum in 64 bits is, the others right."""
+    n, k, group = 300, 512, 64
+    w = _weight(nf4, n, k, group, False, _power_of_two(scale), 3)
+    w.scale[2, 5], w.scale[0, 7], w.scale[7, 200] = float("inf"), float("nan"), float("-inf")
+    x = torch.ones(512, k, device="cuda").bfloat16()
+    x[:256, 128:192] = 0
+    x[:, 129] = 1  # of group 2 the first half of the rows has one weight
+    w64 = nf4.nf4_int4_dequantize(w, torch.float32).double()
+    ref = (x.double().cpu() @ w64.t().cpu()).cuda()
+    for dtype in (torch.float32, torch.bfloat16):
+        y = nf4.nf4_int4_linear(x, w, dtype).double()
+        fine = [r for r in range(n) if r not in (5, 7, 200)]
+        assert torch.equal(y[:, fine], ref[:, fine].to(dtype).double())
+        assert not torch.isfinite(y[:, [5, 7, 200]]).any() and torch.isnan(y[:, 7]).all()

@@ -42,7 +42,7 @@ extern "C" int plan_pass(int64_t m, int64_t n, int64_t k, int64_t group, int sms
 }
 extern "C" int plan_gemm(int64_t m, int64_t n, int64_t k, int sms, int most, int64_t* out) {
     gemm::Plan p;
-    const cudaError_t e = gemm::plan_int4(m, n, k, Device{sms, most}, &p);
+    const cudaError_t e = gemm::plan_int4(m, n, k, 1, Device{sms, most}, &p);
     const int64_t v[3] = {p.rows, p.splits, p.us < 1e29};
     for (int i = 0; i < 3; ++i) out[i] = v[i];
     return e;
