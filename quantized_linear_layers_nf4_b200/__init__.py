@@ -560,6 +560,8 @@ def nf4_int4_linear(X: torch.Tensor, weight: Int4Weight, dtype=torch.bfloat16, o
             out = torch.empty(m, weight.n, dtype=dtype, device=dev)
     else:
         _check_out(out, (m, weight.n), _DTYPES, dev, "out")
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.device != dev or dev_status.numel() < 1):
+        raise ValueError("dev_status must be an int32 tensor on the device of X")
     flags |= _lib.NF4_LINEAR_WEIGHTS_EARLY if weights_early else 0
     _launch(dev.index, stream, _lib.lib().nf4_int4_linear, "nf4_int4_linear", X.data_ptr(), m, weight._struct_ref()[2], out.data_ptr(),
             _DTYPES[out.dtype], None if dev_status is None else dev_status.data_ptr(), flags)

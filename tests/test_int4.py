@@ -409,3 +409,17 @@ def test_binding_refusals_on_device(nf4):
         nf4.nf4_int4_linear(torch.empty(0, 128, device="cuda").bfloat16(), w)
     with pytest.raises(nf4.NF4Error):  # not 16-byte aligned
         nf4.nf4_int4_linear(torch.empty(257, device="cuda").bfloat16()[1:].view(2, 128), w)
+
+
+def test_status_refusals(nf4, monkeypatch):
+    """A status that the kernel could not write (it does so when a wait runs out) is refused before
+    anything is launched."""
+    monkeypatch.setattr(nf4, "_need_cuda", lambda t, name: None)
+    monkeypatch.setattr(nf4, "_launch", lambda *args: None)
+    w = object.__new__(nf4.Int4Weight)
+    w.__dict__.update(n=8, k=64, group=64, wq=torch.zeros(256, dtype=torch.uint8), scale=torch.zeros(1, 8), zero=None)
+    x = torch.zeros(2, 64).bfloat16()
+    for bad in (torch.zeros(1, dtype=torch.int64), torch.zeros(1), torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError):
+            nf4.nf4_int4_linear(x, w, dev_status=bad)
+    nf4.nf4_int4_linear(x, w, dev_status=torch.zeros(1, dtype=torch.int32))
