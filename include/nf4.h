@@ -561,9 +561,11 @@ nf4_status_t nf4_int4_linear(const void* X, int64_t m, const nf4_int4_weight_t* 
  * G_e in rows 2 f e .. 2 f e + f - 1 and U_e in the f rows behind them, down [E * h, f]
  * holds D_e in rows h e .. h e + h - 1.  Weights are used as they stand in their 4 bits,
  * never rounded to bf16 as products; sums, softmax and activations are fp32, and the
- * operands of the tensor cores have 11 significant bits (X all of its bits).  The result
- * does not depend on timing; on the other rows of X it depends in the order of its sums
- * and the rounding of operands alone.
+ * operands of the tensor cores have 11 significant bits: integer codes all of theirs, X too but
+ * for values below 2^-31 of the largest of their row (as for nf4_int4_linear; the router
+ * takes X as it is).  Scales or absmax values of 2^93 or more may overflow sums on the way.
+ * The result does not depend on timing; on the other rows of X it depends in the order of its
+ * sums and the rounding of operands alone.
  */
 #define NF4_MOE_MAX_EXPERTS 512
 #define NF4_MOE_MAX_TOP_K 16

@@ -24,9 +24,10 @@
 //   kG64   groups of 64: 8 consecutive bytes of each half
 //   kG32   groups of 32: 4 consecutive bytes of each quarter
 //   kTable codebook levels with the absmax of each 64: as kG64
-// The copies and what feeds them reach 5.4 TB/s without the products; what the products add is the
-// issue of about 9 instructions a word of codes (integer), or a look-up a byte in a table in shared
-// memory (codebook: L1's data pipe is 70 % busy over a whole kernel, 84 % at its best).
+// The copies and what feeds them reach 5.4 TB/s without the products; what the products add is
+// about 9 instructions a word of codes (integer), or a look-up a byte in a table in shared
+// memory (codebook: L1's data pipe is 70 % busy over a whole kernel, 84 % at its best), beside the
+// steps' own bookkeeping (all in all 150 to 250 instructions a step).
 // Scales go to registers, four groups of a row at a time (a window: kG128 four steps, kG64 and
 // kTable two, kG32 one): lane (g, t) loads that of group t for its rows, one window ahead, and a
 // shuffle hands it to the other lanes of the row.

@@ -33,8 +33,9 @@
 // weight rows and k is split over a cluster of up to 8 CTAs, as the number of tiles asks
 // (plan_int4 in nf4_int4_plan.h), the threads of a team share a small tile's rows, and the CTAs' sums are added in rank
 // order through distributed shared memory; and up to 128 tokens only half of the token tile is
-// multiplied.  512 tokens over 11008 x 4096 take 45 us (1026 TFLOP/s; with one team and 256 rows 60),
-// 128 over 4096 x 4096 14 us.  A stage takes 750 to 1300 cycles, of which the MMAs are 128 to 1024: bound by what a
+// multiplied.  512 tokens over 11008 x 4096 take 45.5 us (1015 TFLOP/s; with one team and 256 rows 60) in
+// short runs at 1965 MHz, and 53 (875 TFLOP/s) in long ones, where the power limit holds the clock at
+// 1680 MHz; 128 over 4096 x 4096 14 us.  A stage takes 750 to 1300 cycles, of which the MMAs are 128 to 1024: bound by what a
 // decoding warp has to issue and wait for.
 // Every mbarrier wait is bounded; a wait that runs out records
 // NF4_ERR_DEVICE_TIMEOUT, the CTA drains what it issued and frees its tensor

@@ -20,8 +20,11 @@
 // writes the rows' scales together.  Its quotient is Markstein's (nf4_encode.cuh), a clamp
 // and an addition of 1.5 * 2^23 round it, and the eight integers of a word, in the low bits
 // of those sums, are put together by one multiply-add each, the excess of all taken off
-// at the end.  Over 11008 x 4096 in bf16, groups of 128, it takes 26 us (4.3 TB/s of 113 MB: the issue
-// of instructions counts as well), with one row a warp and divisions 78.  Dequantization gives a thread the same word of eight rows; a nibble under
+// at the end.  Over 11008 x 4096 in bf16, groups of 128, it takes 32 us (3.5 TB/s of 113 MB, 70 % of the
+// issue slots and 62 % of the ALU pipe used; asymmetric 36), and 49 with the restoration behind it, which
+// finds codes in L2; with one row a warp and divisions those two took 115.  Groups of no power of two
+// (k_int4_quantize_any) read W twice: 68 us over 11008 x 3840 in groups of 192, 29 in groups of 128.
+// Dequantization gives a thread the same word of eight rows; a nibble under
 // the mantissa of 2^23 needs no shift, since its power of 16 goes into the scale: 21.9 us
 // (5.2 TB/s, 81 % of the rate of a copy), with one row a thread 37.
 #include "nf4_common.cuh"
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(256) k_int4_quantize(const void* __restrict__ 
         }
         // Two halvings of the lanes halve the rows each keeps, so a row's extremes end in a quarter of
         // its lanes, which make its scale for all: with all rows reduced in all lanes it took 16
-        // shuffles a lane in place of 5, and 51 us (with a restoration, 11008 x 4096) in place of 48.
+        // shuffles a lane in place of 5, and 3 us more (with a restoration, 11008 x 4096).
         float lo[kLoads], hi[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) v[i].template extremes<kZero>(lo[i], hi[i]);

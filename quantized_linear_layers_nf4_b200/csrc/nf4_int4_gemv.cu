@@ -14,8 +14,10 @@
 // memory, so results do not depend on timing.
 //
 // Groups of 128, bf16 scales: one token over 4096 x 4096 takes 6.2 us, of which a launch and X are
-// 4, over 28672 x 8192 27.4 us (4.4 TB/s, 69 % of the rate of a copy); sixteen tokens 42.4 us there,
-// bound by the issue of instructions (48.3 with groups of 64 and zero points).
+// 4, over 28672 x 8192 27.4 us (4.4 TB/s, 69 % of the rate of a copy); sixteen tokens 44.5 us there
+// (48.2 with groups of 64 and zero points).  No unit is full then: a step (16 rows x 128 k) is 202 warp
+// instructions (247; one token 151), of which decoding is 72 and products 16, and they fill 57 % (61 %;
+// 63 %) of the issue slots with the four warps that a scheduler has.
 #include "nf4_few.cuh"
 #include "nf4_int4_plan.h"
 #include "nf4_ptx.cuh"

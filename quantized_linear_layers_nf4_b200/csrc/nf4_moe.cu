@@ -8,7 +8,7 @@
 // Bound by HBM: each chosen expert's three matrices are read once, whoever shares it.
 // Three launches, each a programmatic dependent of the one before:
 //   k_moe_router   one dot product per (expert, token), and X as fp16 times a power of two
-//   k_moe_gate_up  every CTA chooses the experts itself from the logits (cheaper than
+//   k_moe_gate_up  every CTA chooses the experts itself from the logits (which saves
 //                  another launch), then takes its share of the (expert, 8 rows of f)
 //                  tiles: 8 gate rows and the 8 up rows that belong to them form the 16
 //                  rows of one mma.sync tile, so a lane holds a gate sum and its up sum
@@ -17,12 +17,15 @@
 // The weights' decoding and the step geometry are in nf4_few.cuh.  Every sum is taken in a
 // fixed order.
 //
-// NF4: one token of 64 experts (6 chosen, 2048 x 1408) takes 24 us, of which the launches and the
-// routing are about 10; sixteen tokens of 8 experts (2 chosen, 4096 x 14336) 256 us, 2.8 TB/s: the
-// table look-ups bound it (the copies alone, at 5.4 TB/s, would take 134 us).  Integer codes: 7 tokens of 128
-// experts (8 chosen, 2048 x 768) 44.7 us, 2.5 TB/s.
+// NF4: one token of 64 experts (6 chosen, 2048 x 1408) takes 25 us, of which the launches and the
+// routing are about 10; sixteen tokens of 8 experts (2 chosen, 4096 x 14336) 256 us, 2.8 TB/s: L1's
+// data pipe is 70 % busy, about half of that with table look-ups, the rest with X and the codes' way
+// through the ring (the copies alone, at 5.4 TB/s, would take 134 us).  Integer codes: 7 tokens of 128
+// experts (8 chosen, 2048 x 768) 45 us, 2.5 TB/s; 54 % of the issue slots are used and no pipe more.
+// Above sixteen tokens a pass reads its experts again: 32 tokens of those 8 experts 526 us.
 //
-// Roundings.  X (bf16) times a power of two per token is exact in fp16.  Codebook levels
+// Roundings.  X (bf16) times a power of two per token is exact in fp16, but for values below
+// 2^-31 of the token's largest.  Codebook levels
 // are rounded to fp16 (within 2^-11 of the value; bf16 would be 2^-8, as much as the rounding
 // of the result); integer codes are exact.  The activations a are kept in fp32 and, for the
 // products, rounded to fp16 (2^-11); where a token's largest one is outside [2^-6, 2^15)
