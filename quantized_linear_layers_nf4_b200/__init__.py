@@ -159,7 +159,7 @@ class _KeptStruct:
         if kept is None or kept[0] != key:
             st = self._make(key)
             kept = (key, st, ctypes.byref(st))
-            object.__setattr__(self, "_kept", kept)
+            _set_kept(self, kept)
         return kept
 
     def struct(self):
@@ -168,6 +168,9 @@ class _KeptStruct:
 
     def __getstate__(self):
         return self.__dict__
+
+
+_set_kept = _KeptStruct._kept.__set__  # past a frozen class's own
 
 
 @dataclass
@@ -482,6 +485,23 @@ class Int4Weight(_KeptStruct):
                 (0 if self.zero is None else self.zero.numel()))
 
 
+def _int4_outputs(n, k, group, symmetric, scale_dtype, wq, scale, zero, dev):
+    """The outputs of a quantization: those given, checked, and new ones."""
+    if wq is None:
+        wq = torch.empty(n * k // 2, dtype=torch.uint8, device=dev)
+    else:
+        _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
+    if scale is None:
+        scale = torch.empty(k // group, n, dtype=scale_dtype, device=dev)
+    else:
+        _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
+    if zero is not None:
+        _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
+    elif not symmetric:
+        zero = torch.empty(k // group, n, dtype=torch.uint8, device=dev)
+    return wq, scale, zero
+
+
 def nf4_int4_quantize(W: torch.Tensor, group: int = 128, symmetric: bool = True, scale_dtype=torch.bfloat16,
                       wq: torch.Tensor | None = None, scale: torch.Tensor | None = None,
                       zero: torch.Tensor | None = None, stream=None):
@@ -498,19 +518,11 @@ def nf4_int4_quantize(W: torch.Tensor, group: int = 128, symmetric: bool = True,
     if not _group_ok(k, group):
         raise ValueError(_GROUP_RULE)
     dev = W.device
-    with _memory_of(stream):
-        if wq is None:
-            wq = torch.empty(n * k // 2, dtype=torch.uint8, device=dev)
-        else:
-            _check_out(wq, (n * k // 2,), (torch.uint8,), dev, "wq")
-        if scale is None:
-            scale = torch.empty(k // group, n, dtype=scale_dtype, device=dev)
-        else:
-            _check_out(scale, (k // group, n), (scale_dtype,), dev, "scale")
-        if zero is not None:
-            _check_out(zero, (k // group, n), (torch.uint8,), dev, "zero")
-        elif not symmetric:
-            zero = torch.empty(k // group, n, dtype=torch.uint8, device=dev)
+    if stream is None:
+        wq, scale, zero = _int4_outputs(n, k, group, symmetric, scale_dtype, wq, scale, zero, dev)
+    else:
+        with _memory_of(stream):
+            wq, scale, zero = _int4_outputs(n, k, group, symmetric, scale_dtype, wq, scale, zero, dev)
     _launch(dev.index, stream, _lib.lib().nf4_int4_quantize, "nf4_int4_quantize", W.data_ptr(), _DTYPES[W.dtype], n, k, group,
             _DTYPES[scale_dtype], wq.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
     return wq, scale, zero
@@ -530,8 +542,11 @@ def nf4_int4_dequantize(weight: Int4Weight, dtype=torch.bfloat16, out: torch.Ten
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError("dtype must be float32 or bfloat16")
-        with _memory_of(stream):
+        if stream is None:
             out = torch.empty(weight.n, weight.k, dtype=dtype, device=dev)
+        else:
+            with _memory_of(stream):
+                out = torch.empty(weight.n, weight.k, dtype=dtype, device=dev)
     else:
         _check_out(out, (weight.n, weight.k), _DTYPES, dev, "out")
     _launch(dev.index, stream, _lib.lib().nf4_int4_dequantize, "nf4_int4_dequantize", weight._struct_ref()[2], out.data_ptr(),
